@@ -175,7 +175,6 @@ def _prepare_pages(case, seed):
         ring[(head + np.arange(n_blocks - n_owned)) % n_blocks] = ids[n_owned:]
         s.update(lens=_i32(pl["ctx"] + pl["new"]), table=_i32(table), owned=_i32(pl["owned"]), ring=_i32(ring),
                  pool=_i32([head, n_blocks - n_owned]), owned_out=_i32(np.zeros(B)), pool_out=_i32([0, 0]))
-        s["ws"] = torch.zeros(64 + 16 * B, dtype=torch.uint8, device=DEV)
         return s
     table[np.arange(mb)[None, :] < pl["need"][:, None]] = ids[:n_need]
     rows = pl["budget"]   # the buffers' size; rows behind the last sequence stay as they were
@@ -272,8 +271,8 @@ def run(state):
         return state["out_lp"]
     if op == "blocks":
         bi.bi_block_table_resize(state["lens"], c["B"], state["table"], c["max_blocks"], state["owned"],
-                                 state["ring"], state["n_blocks"], state["pool"], workspace=state["ws"],
-                                 n_owned_out=state["owned_out"], pool_out=state["pool_out"])
+                                 state["ring"], state["n_blocks"], state["pool"], n_owned_out=state["owned_out"],
+                                 pool_out=state["pool_out"])
         return state["table"], state["owned_out"], state["pool_out"]
     bi.bi_slot_map(state["new"], state["start"], c["B"], state["table"], c["max_blocks"], state["n_blocks"],
                    state["rows"], state["row0"], state["row_seq"], state["row_pos"], state["slots"])
