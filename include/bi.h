@@ -70,7 +70,7 @@ const char* bi_last_error(void);
 int64_t bi_launch_count(void);
 /* Synchronises the current device, then returns BI_OK, BI_ERR_TIMEOUT (a
  * bounded device wait gave up) or BI_ERR_DEVICE_CHECK (a kernel saw an
- * out-of-range index) and clears the device status word. */
+ * out-of-range index or value) and clears the device status word. */
 bi_status bi_device_status(void);
 
 /* ------------------------------------------------------------------ RMSNorm
@@ -159,6 +159,44 @@ bi_status bi_qkv_rope_kv_write(const void* x, int64_t T, int64_t K, const void* 
 /* rope_table[p, i] = cos(p * theta^(-2i/hd)), rope_table[p, hd/2 + i] = sin(...),
  * angles and functions evaluated in fp64 on the device, rounded to fp32. */
 bi_status bi_rope_table(float* rope_table, int64_t max_pos, int hd, double theta, void* stream);
+
+/* ------------------------------------------------- paged-cache planning
+ * [Article] §4.2 (every phase writes and reads K/V through the block table),
+ * §4.6 (a captured step reads nothing back to the host).
+ *
+ * bi_block_table_resize: request b gets the blocks that
+ * ceil((lens[b] + extra) / 64) asks for (0 when lens[b] <= 0): missing ones
+ * are taken from the pool in request order and written behind its
+ * n_owned[b] entries of block_table [B, max_blocks_per_seq]; surplus ones go
+ * back to the pool and their entries become -1.  The pool is a ring: pool
+ * (device int32 [2]) = (head, count), the free ids being ring[(head + i) %
+ * n_blocks], i < count (ring: device int32 [n_blocks]).  Blocks given back in a
+ * call are handed out by later calls only.  The result depends on the lengths
+ * alone.  A request that the pool cannot serve after the requests before it
+ * (counting those that failed), or that needs more than max_blocks_per_seq
+ * blocks, keeps what it has and sets the device status; n_owned_out tells
+ * which.  n_owned_out [B] and pool_out [2] receive the new counts: the inputs
+ * themselves, or other arrays (the table and the ring change either way).
+ * lens, n_owned: device int32 [B].  extra in [0, 2^31) is added to every
+ * positive length (a decode step passes its positions and extra = 1).
+ *
+ * bi_slot_map: the packed rows of a step in which request b adds
+ * new_tokens[b] >= 0 tokens at positions start[b], start[b] + 1, ... (device
+ * int32 [B] both): row0 [B + 1] (the first row of each request, then the
+ * number of rows: bi_attention's piece_row0, with start as its piece_pos0),
+ * and per row the request, the position (bi_qkv_rope_kv_write's row_seq and
+ * row_pos) and the cache slot block_table[request, position / 64] * 64 +
+ * position % 64 (int64).  row_seq, row_pos and slots hold T rows and may each
+ * be NULL (block_table may be, without slots).  Rows behind the last request's
+ * stay as they were.  More than T rows: those beyond are left out, row0 is cut
+ * at T, and the device status is set, as it is for a position without a block
+ * (slot -1). */
+bi_status bi_block_table_resize(const int32_t* lens, int64_t extra, int64_t B, int32_t* block_table,
+                                int64_t max_blocks_per_seq, const int32_t* n_owned, int32_t* ring, int64_t n_blocks,
+                                const int32_t* pool, int32_t* n_owned_out, int32_t* pool_out, void* stream);
+bi_status bi_slot_map(const int32_t* new_tokens, const int32_t* start, int64_t B, const int32_t* block_table,
+                      int64_t max_blocks_per_seq, int64_t n_blocks, int64_t T, int32_t* row0, int32_t* row_seq,
+                      int32_t* row_pos, int64_t* slots, void* stream);
 
 /* ---------------------------------------------------------------- attention
  * [Article] §4.2 (one read path for prefill and decode; decode's default
@@ -390,6 +428,51 @@ bi_status bi_lm_head_logprob(const void* X, int64_t T, int64_t K, const void* W,
                              float* logprob_out, int32_t* argmax_out, int mode, void* workspace, size_t ws_bytes,
                              void* stream);
 size_t bi_lm_head_logprob_workspace_size(int64_t T, int64_t V, int64_t K, int mode);
+
+/* ----------------------------------------------------------------- sampling
+ * [Article] §2 ("the same discrete choices", batch independence): a sampled
+ * token and its logprob are the row's own, whatever the batch, and the
+ * recompute of that logprob gives the same bits.
+ * For a row x of V logits at temperature T > 0, with masses
+ * w_i = exp((x_i - max x) / T) and the tokens in the order (x descending, index
+ * ascending), the kept set is a prefix of that order, cut in turn by
+ *   min_p: w_i >= min_p (of the largest, 1);
+ *   top_k: the first top_k tokens of what is left;
+ *   top_p: the shortest prefix of what is left with at least top_p of its mass.
+ * bi_sample draws, for a given u in [0, 1), the first token in index order
+ * whose running kept mass exceeds u times the kept mass S; its logprob is
+ * (x_i - max x) / T - ln S.  T = 0 is greedy: the first maximum, logprob 0.
+ * bi_sample_logprob gives the same logprob (the same bits) of a given token, or
+ * -inf for one that is not kept.  Masses are held to about 3e-10 and summed as
+ * integers, so results depend neither on T (the row count) nor on the batch.
+ *
+ * bi_sampling: device arrays of n entries each, or NULL: temperature (NULL: 1;
+ * 0, or 2^-64 to 2^64), top_k (NULL, <= 0 or >= V: off), top_p (NULL or >= 1:
+ * off; <= 0: one token), min_p (NULL or <= 0: off; >= 1: the maxima only).  Row
+ * t uses entry param_row[t] (device int32 [T]), or entry t when param_row is
+ * NULL (then n >= T).  A NULL bi_sampling is temperature 1 with no cut.
+ * logits: fp32 or bf16 (dtype) [T, V] with row stride ld >= V elements, aligned
+ * to their type only (any ld).  1 <= V <= 262144.  -inf logits are never drawn
+ * and have no mass; they need no mask of their own.
+ * u: fp32 [u_rows, T]; the call reads row *u_row (device int32 [1]), or row 0
+ * when u_row is NULL, so that a captured decode step can walk its random
+ * numbers.  ids_out: int32 [T]; logprob_out: fp32 [T] or NULL (bi_sample).
+ * A row of -inf alone gives id -1 and logprob -inf.  A row that holds NaN or
+ * +inf, or whose parameters, id or u are out of range, gives id -1 (bi_sample)
+ * and logprob NaN and sets the device status; other rows are not touched. */
+typedef struct {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int64_t n;
+} bi_sampling;
+bi_status bi_sample(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, const bi_sampling* sampling,
+                    const int32_t* param_row, const float* u, int64_t u_rows, const int32_t* u_row, int32_t* ids_out,
+                    float* logprob_out, void* stream);
+bi_status bi_sample_logprob(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                            const bi_sampling* sampling, const int32_t* param_row, const int32_t* ids,
+                            float* logprob_out, void* stream);
 
 /* ---------------------------------------------------------------------- MoE
  * Router: [Article] §2 "the same discrete choices", §4.4 (router output fp32

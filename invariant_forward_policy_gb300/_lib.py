@@ -58,6 +58,25 @@ class bi_weights(ctypes.Structure):
                 ("rope_table", _vp)]
 
 
+class bi_sampling(ctypes.Structure):
+    """Sampling parameters: device tensors of n entries each (fp32, int32 for top_k), or None."""
+    _fields_ = [("temperature", _vp), ("top_k", _vp), ("top_p", _vp), ("min_p", _vp), ("n", _i64)]
+
+    def __init__(self, temperature=None, top_k=None, top_p=None, min_p=None):
+        arrays = (temperature, top_k, top_p, min_p)
+        n = None
+        for t, kind in zip(arrays, (torch.float32, torch.int32, torch.float32, torch.float32)):
+            if t is None:
+                continue
+            if t.dtype != kind or not t.is_contiguous():
+                raise ValueError("sampling parameters are contiguous fp32 tensors (int32 for top_k)")
+            if n is not None and t.numel() != n:
+                raise ValueError("sampling parameters of different lengths")
+            n = t.numel()
+        super().__init__(_p(temperature), _p(top_k), _p(top_p), _p(min_p), n or 0)
+        self.tensors = arrays   # the structure holds addresses only
+
+
 _SIGS = {
     "bi_version": (_int, []),
     "bi_last_error": (ctypes.c_char_p, []),
@@ -73,6 +92,8 @@ _SIGS = {
     "bi_rope_table": (_int, [_vp, _i64, _int, _f64, _vp]),
     "bi_qkv_rope_kv_write": (_int, [_vp, _i64, _i64, _vp, _int, _int, _int, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _vp,
                                     _vp, _vp, _int, _vp]),
+    "bi_block_table_resize": (_int, [_vp, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp]),
+    "bi_slot_map": (_int, [_vp, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
     "bi_attention": (_int, [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _int, _int, _int, _vp, _vp, _vp, _i64, _i64, _i64,
                             _int, _f32, _vp, _sz, _vp, _int, _vp]),
     "bi_attention_workspace_size": (_sz, [_i64, _int, _int, _i64, _int]),
@@ -97,6 +118,9 @@ _SIGS = {
     "bi_logprob_workspace_size": (_sz, [_i64, _i64, _int]),
     "bi_lm_head_logprob": (_int, [_vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _int, _vp, _sz, _vp]),
     "bi_lm_head_logprob_workspace_size": (_sz, [_i64, _i64, _i64, _int]),
+    "bi_sample": (_int, [_vp, _int, _i64, _i64, _i64, ctypes.POINTER(bi_sampling), _vp, _vp, _i64, _vp, _vp, _vp,
+                         _vp]),
+    "bi_sample_logprob": (_int, [_vp, _int, _i64, _i64, _i64, ctypes.POINTER(bi_sampling), _vp, _vp, _vp, _vp]),
     "bi_moe_route_topk": (_int, [_vp, _i64, _int, _int, _vp, _vp, _vp]),
     "bi_moe_permute": (_int, [_vp, _i64, _int, _int, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
     "bi_moe_permute_workspace_size": (_sz, [_i64, _int, _int]),
@@ -230,6 +254,20 @@ def bi_rope_kv_write(qkv, T, piece_seq, piece_row0, piece_pos0, P, max_q_len, Hq
                                    _p(q_out), _p(k_cache), _p(v_cache), _s(stream)))
 
 
+def bi_block_table_resize(lens, B, block_table, max_blocks_per_seq, n_owned, ring, n_blocks, pool, extra=0,
+                          n_owned_out=None, pool_out=None, stream=None):
+    """n_owned and pool are updated in place unless other outputs are given."""
+    _check(load().bi_block_table_resize(_p(lens), extra, B, _p(block_table), max_blocks_per_seq, _p(n_owned),
+                                        _p(ring), n_blocks, _p(pool), _p(n_owned if n_owned_out is None else n_owned_out),
+                                        _p(pool if pool_out is None else pool_out), _s(stream)))
+
+
+def bi_slot_map(new_tokens, start, B, block_table, max_blocks_per_seq, n_blocks, T, row0, row_seq=None, row_pos=None,
+                slots=None, stream=None):
+    _check(load().bi_slot_map(_p(new_tokens), _p(start), B, _p(block_table), max_blocks_per_seq, n_blocks, T,
+                              _p(row0), _p(row_seq), _p(row_pos), _p(slots), _s(stream)))
+
+
 def bi_attention(q, T, piece_seq, piece_row0, piece_pos0, P, max_q_len, Hq, Hkv, hd, k_cache, v_cache, block_table,
                  max_blocks_per_seq, n_blocks, max_ctx, kv_split, scale, workspace, out, mode=BI_INVARIANT,
                  stream=None):
@@ -328,6 +366,18 @@ def bi_lm_head_logprob(X, T, K, W, V, ids, logprob_out, argmax_out=None, mode=BI
 
 def bi_lm_head_logprob_workspace_size(T, V, K, mode=BI_INVARIANT) -> int:
     return load().bi_lm_head_logprob_workspace_size(T, V, K, mode)
+
+
+def bi_sample(logits, T, V, sampling, u, ids_out, logprob_out=None, dtype=BI_DTYPE_FP32, ld=None, param_row=None,
+              u_rows=1, u_row=None, stream=None):
+    _check(load().bi_sample(_p(logits), dtype, T, V, V if ld is None else ld, sampling, _p(param_row), _p(u), u_rows,
+                            _p(u_row), _p(ids_out), _p(logprob_out), _s(stream)))
+
+
+def bi_sample_logprob(logits, T, V, sampling, ids, logprob_out, dtype=BI_DTYPE_FP32, ld=None, param_row=None,
+                      stream=None):
+    _check(load().bi_sample_logprob(_p(logits), dtype, T, V, V if ld is None else ld, sampling, _p(param_row),
+                                    _p(ids), _p(logprob_out), _s(stream)))
 
 
 def bi_moe_route_topk(logits, T, E, k, ids, weights, stream=None):

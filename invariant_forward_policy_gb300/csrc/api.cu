@@ -162,6 +162,8 @@ bi_status bi_device_status(void) {
   int zero = 0;
   cudaMemcpyToSymbol(bi::g_device_status, &zero, sizeof(int));
   if (v == bi::DEV_TIMEOUT) return bi::fail(BI_ERR_TIMEOUT, "a bounded device wait gave up");
+  if (v == bi::DEV_BAD_VALUE)
+    return bi::fail(BI_ERR_DEVICE_CHECK, "a kernel saw an out-of-range value (code " + std::to_string(v) + ")");
   if (v != 0) return bi::fail(BI_ERR_DEVICE_CHECK, "a kernel saw an out-of-range index (code " + std::to_string(v) + ")");
   return BI_OK;
 }

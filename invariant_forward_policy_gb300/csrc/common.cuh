@@ -46,8 +46,8 @@ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int num_sms();
 
 // Device status word: kernels that give up a bounded wait, or that see an
-// out-of-range index, record a code here instead of trapping.
-enum DeviceCode : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_BAD_INDEX = 2 };
+// out-of-range index or value, record a code here instead of trapping.
+enum DeviceCode : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_BAD_INDEX = 2, DEV_BAD_VALUE = 3 };
 int* device_status_ptr();  // device address of the status word (current device and context)
 
 
