@@ -632,6 +632,34 @@ bi_status bi_forward_decode(bi_model* m, const int32_t* tokens, const int32_t* p
                             int64_t n_blocks, int64_t max_ctx, int32_t* sampled_out, float* logprob_out,
                             void* workspace, size_t ws_bytes, int mode, void* stream);
 
+/* The sampling forms of the two calls above: the same layer stack, then the
+ * lm_head logits in fp32 (bi_gemm) and bi_sample or bi_sample_logprob on them,
+ * so a drawn token's logprob in a decode step, in any batch, has the bits that
+ * the recompute gives it.  `sampling` holds one entry per sequence (n >= B).
+ *  - bi_forward_prefill_sample: exactly one of target_ids (device int32 [T]:
+ *    rows with logits score them; sampled_out is not written) and u (device
+ *    fp32 [T], one per packed row, read at the rows with logits: a draw, into
+ *    sampled_out).
+ *  - bi_forward_decode_sample: u fp32 [u_rows, B], of which the step reads row
+ *    *u_row (device int32; NULL: row 0), e.g. bi_decode_advance's step_counter.
+ * The other arguments are those of bi_forward_prefill / bi_forward_decode, with
+ * a workspace of bi_forward_sample_workspace_size bytes (the plain one plus
+ * max_logit_rows rows of fp32 logits). */
+bi_status bi_forward_prefill_sample(bi_model* m, const int32_t* tokens, const int32_t* target_ids,
+                                    const bi_sampling* sampling, const float* u, const int64_t* cu_seqlens,
+                                    const int64_t* start_pos, const int64_t* logit_from, int64_t B, int64_t chunk,
+                                    const int32_t* block_table, int64_t max_blocks_per_seq, void* k_cache,
+                                    void* v_cache, int64_t n_blocks, float* logprob_out, int32_t* sampled_out,
+                                    void* workspace, size_t ws_bytes, int64_t max_tokens, int64_t max_ctx,
+                                    int64_t max_logit_rows, int mode, void* stream);
+bi_status bi_forward_decode_sample(bi_model* m, const int32_t* tokens, const int32_t* pos, int64_t B,
+                                   const bi_sampling* sampling, const float* u, int64_t u_rows, const int32_t* u_row,
+                                   const int32_t* block_table, int64_t max_blocks_per_seq, void* k_cache,
+                                   void* v_cache, int64_t n_blocks, int64_t max_ctx, int32_t* sampled_out,
+                                   float* logprob_out, void* workspace, size_t ws_bytes, int mode, void* stream);
+size_t bi_forward_sample_workspace_size(const bi_model_config* cfg, int64_t max_tokens, int64_t max_pieces,
+                                        int64_t max_ctx, int64_t max_logit_rows, int mode);
+
 /* Rollout bookkeeping after a decode step (device only, capturable):
  * hist_ids[step, b] = sampled[b], hist_lp[step, b] = logprob[b] with
  * step = *step_counter; then tokens[b] = sampled[b], pos[b] += 1, and

@@ -143,6 +143,12 @@ _SIGS = {
                                ctypes.POINTER(_i64), _i64]),
     "bi_forward_decode": (_int, [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _int,
                                  _vp]),
+    "bi_forward_prefill_sample": (_int, [_vp, _vp, _vp, ctypes.POINTER(bi_sampling), _vp, ctypes.POINTER(_i64),
+                                         ctypes.POINTER(_i64), ctypes.POINTER(_i64), _i64, _i64, _vp, _i64, _vp, _vp,
+                                         _i64, _vp, _vp, _vp, _sz, _i64, _i64, _i64, _int, _vp]),
+    "bi_forward_decode_sample": (_int, [_vp, _vp, _vp, _i64, ctypes.POINTER(bi_sampling), _vp, _i64, _vp, _vp, _i64,
+                                        _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _int, _vp]),
+    "bi_forward_sample_workspace_size": (_sz, [ctypes.POINTER(bi_model_config), _i64, _i64, _i64, _i64, _int]),
     "bi_decode_advance": (_int, [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
 }
 
@@ -480,6 +486,33 @@ def bi_forward_decode(model, tokens, pos, B, block_table, max_blocks_per_seq, k_
     _check(load().bi_forward_decode(model, _p(tokens), _p(pos), B, _p(block_table), max_blocks_per_seq, _p(k_cache),
                                     _p(v_cache), n_blocks, max_ctx, _p(sampled_out), _p(logprob_out), _p(workspace),
                                     _nb(workspace), mode, _s(stream)))
+
+
+def bi_forward_prefill_sample(model, tokens, target_ids, sampling, u, cu_seqlens, start_pos, logit_from, B, chunk,
+                              block_table, max_blocks_per_seq, k_cache, v_cache, n_blocks, logprob_out, sampled_out,
+                              workspace, max_tokens, max_ctx, max_logit_rows, mode=BI_INVARIANT, stream=None):
+    cu = _i64_array(cu_seqlens)
+    sp = _i64_array(start_pos)
+    lf = _i64_array(logit_from)
+    _check(load().bi_forward_prefill_sample(model, _p(tokens), _p(target_ids), sampling, _p(u), cu, sp, lf, B, chunk,
+                                            _p(block_table), max_blocks_per_seq, _p(k_cache), _p(v_cache), n_blocks,
+                                            _p(logprob_out), _p(sampled_out), _p(workspace), _nb(workspace),
+                                            max_tokens, max_ctx, max_logit_rows, mode, _s(stream)))
+
+
+def bi_forward_decode_sample(model, tokens, pos, B, sampling, u, block_table, max_blocks_per_seq, k_cache, v_cache,
+                             n_blocks, max_ctx, sampled_out, logprob_out, workspace, u_rows=1, u_row=None,
+                             mode=BI_INVARIANT, stream=None):
+    _check(load().bi_forward_decode_sample(model, _p(tokens), _p(pos), B, sampling, _p(u), u_rows, _p(u_row),
+                                           _p(block_table), max_blocks_per_seq, _p(k_cache), _p(v_cache), n_blocks,
+                                           max_ctx, _p(sampled_out), _p(logprob_out), _p(workspace), _nb(workspace),
+                                           mode, _s(stream)))
+
+
+def bi_forward_sample_workspace_size(cfg: bi_model_config, max_tokens, max_pieces, max_ctx, max_logit_rows,
+                                     mode=BI_INVARIANT) -> int:
+    return load().bi_forward_sample_workspace_size(ctypes.byref(cfg), max_tokens, max_pieces, max_ctx, max_logit_rows,
+                                                   mode)
 
 
 def bi_decode_advance(sampled, logprob, tokens, pos, B, step_counter, hist_ids, hist_lp, max_steps, stream=None):

@@ -100,6 +100,12 @@ bi_status lm_head_logprob_to(const void* X, int64_t T, int64_t K, const void* W,
                              float* logprob_out, int32_t* argmax_out, const int32_t* dst, int mode, void* workspace,
                              size_t ws_bytes, void* stream);
 size_t lm_head_partial_bytes(int64_t T, int64_t V, int64_t K, int mode);
+constexpr int64_t kMaxSampleVocab = 262144;
+// Token draw (u) or scoring (ids_in) of T fp32 logit rows [T, V]: row r belongs to index dst[r] of u,
+// ids_out and lp_out, and uses entry param_row[r] of `sampling`.
+bi_status sample_rows(const float* logits, int64_t T, int64_t V, const bi_sampling* sampling, const int32_t* param_row,
+                      const float* u, int64_t u_ld, int64_t u_rows, const int32_t* u_row, const int32_t* ids_in,
+                      const int32_t* dst, int32_t* ids_out, float* lp_out, cudaStream_t st);
 // QKV projection whose epilogue applies RoPE (q, k) and writes k, v into the
 // paged cache at each row's (row_seq, row_pos): the same values as bi_gemm
 // followed by bi_rope_kv_write, without the bf16 qkv round trip.

@@ -48,6 +48,15 @@ struct DevMeta {
   int32_t* logit_tgt;  // target id of each logit row (or -1)
   int32_t* row_seq;    // sequence of every pass row
   int32_t* row_pos;    // absolute position of every pass row
+  int32_t* logit_seq;  // sequence of each logit row (sampling calls; NULL otherwise)
+};
+
+// The head of a sampling call: logits in memory, then a draw (u) or the score of the targets.
+struct SampleHead {
+  const bi_sampling* params;  // one entry per sequence
+  const float* u;             // [u_rows, u_ld], at the call's row indices; NULL: score the targets
+  int64_t u_ld, u_rows;
+  const int32_t* u_row;
 };
 
 __global__ void pass_meta_kernel(const PassMeta pm, const int32_t* __restrict__ tokens,
@@ -79,6 +88,7 @@ __global__ void pass_meta_kernel(const PassMeta pm, const int32_t* __restrict__ 
     const int j = pm.loff[p] + (i - pm.lfirst[p]);
     dm.logit_src[j] = r;
     dm.logit_dst[j] = tok;
+    if (dm.logit_seq) dm.logit_seq[j] = pm.seq[p];
     dm.logit_tgt[j] = targets ? targets[tok] : -1;
   }
 }
@@ -102,6 +112,7 @@ __global__ void decode_embed_kernel(const int32_t* __restrict__ tokens, const in
     dm.row_pos[b] = pos[b];
     dm.logit_src[b] = b;
     dm.logit_dst[b] = b;
+    if (dm.logit_seq) dm.logit_seq[b] = b;
     dm.logit_tgt[b] = -1;
   }
   const bool ok = id >= 0 && id < V;
@@ -122,10 +133,13 @@ struct FwdLayout {
   size_t attn_ws_bytes, gemm_ws_bytes, lp_ws_bytes;
   // fp8 only: bf16 qkv and gate/up outputs, activation codes and scales
   size_t qkv, g13, qa, sa;
+  // sampling calls only: the logit rows' sequences and fp32 logits
+  size_t logit_seq, head_logits;
   size_t total;
 };
 
-static FwdLayout plan_layout(const bi_model_config& c, int64_t Tm, int64_t Pm, int64_t max_ctx, int64_t Rm, int mode) {
+static FwdLayout plan_layout(const bi_model_config& c, int64_t Tm, int64_t Pm, int64_t max_ctx, int64_t Rm, int mode,
+                             bool sample = false) {
   FwdLayout L{};
   size_t off = 0;
   auto take = [&](size_t n) {
@@ -168,6 +182,7 @@ static FwdLayout plan_layout(const bi_model_config& c, int64_t Tm, int64_t Pm, i
     g = std::max(g, bi_gemm_workspace_size(m, c.d, hq, BI_EPI_NONE, mode));
     g = std::max(g, bi_gemm_workspace_size(m, 2 * c.ffn, c.d, BI_EPI_SWIGLU, mode));
     g = std::max(g, bi_gemm_workspace_size(m, c.d, c.ffn, BI_EPI_NONE, mode));
+    if (sample) g = std::max(g, bi_gemm_workspace_size(m, c.vocab, c.d, BI_EPI_NONE, mode));
   }
   L.gemm_ws_bytes = g;
   L.gemm_ws = take(g);
@@ -177,6 +192,10 @@ static FwdLayout plan_layout(const bi_model_config& c, int64_t Tm, int64_t Pm, i
     L.g13 = take(Tm * 2 * c.ffn * 2);
     L.qa = take(Tm * kmax);
     L.sa = take(Tm * (kmax / 128) * 4);
+  }
+  if (sample) {
+    L.logit_seq = take(std::max(Tm, Rm) * 4);
+    L.head_logits = take((size_t)Rm * c.vocab * 4);
   }
   L.total = off + 256;
   return L;
@@ -266,7 +285,7 @@ static std::vector<PassPlan> plan_prefill(const int64_t* cu_seqlens, const int64
 static bi_status run_pass(bi_model* m, void* ws, const FwdLayout& L, const PassShape& ps, int64_t Rm,
                           const int32_t* block_table, int64_t max_blk, void* k_cache, void* v_cache,
                           int64_t n_blocks, bool greedy, float* logprob_out, int32_t* sampled_out, int mode,
-                          void* stream) {
+                          void* stream, const SampleHead* sample = nullptr) {
   const bi_model_config& c = m->cfg;
   const int64_t T = ps.rows;
   const int64_t nqkv = (c.n_heads_q + 2 * c.n_heads_kv) * c.head_dim;
@@ -392,12 +411,21 @@ static bi_status run_pass(bi_model* m, void* ws, const FwdLayout& L, const PassS
     void* xsel = at<void>(ws, L.xsel);
     // rows src[j] of (down-proj out + residual) -> final norm -> compact row j
     BI_TRY(rmsnorm_rows(tmp, res, m->final_norm, xsel, R, c.d, c.eps, src, stream));
+    if (sample) {
+      float* logits = at<float>(ws, L.head_logits);
+      BI_TRY(bi_gemm(xsel, R, c.d, m->lm_head, c.vocab, logits, BI_DTYPE_FP32, BI_EPI_NONE, mode, gws, L.gemm_ws_bytes,
+                     stream));
+      BI_TRY(sample_rows(logits, R, c.vocab, sample->params, at<int32_t>(ws, L.logit_seq) + r0, sample->u,
+                         sample->u_ld, sample->u_rows, sample->u_row,
+                         sample->u ? nullptr : at<int32_t>(ws, L.logit_tgt) + r0, at<int32_t>(ws, L.logit_dst) + r0,
+                         sampled_out, logprob_out, st));
+      continue;
+    }
     // lm_head + log-softmax + gather fused; results land at the call's row index
     const int32_t* tgt = greedy ? nullptr : at<int32_t>(ws, L.logit_tgt) + r0;
     BI_TRY(lm_head_logprob_to(xsel, R, c.d, m->lm_head, c.vocab, tgt, logprob_out, sampled_out,
                               at<int32_t>(ws, L.logit_dst) + r0, mode, at<void>(ws, L.logits), L.lp_ws_bytes, stream));
   }
-  (void)st;
   return BI_OK;
 }
 
@@ -420,6 +448,15 @@ static bi_status validate_cfg(const bi_model_config* c) {
     BI_REQUIRE_SHAPE(c->d % 128 == 0 && c->ffn % 128 == 0 && (c->n_heads_q * c->head_dim) % 128 == 0 &&
                          ((c->n_heads_q + 2 * c->n_heads_kv) * c->head_dim) % 128 == 0,
                      "fp8 needs d, ffn, Hq*hd and (Hq + 2 Hkv)*hd multiples of 128");
+  return BI_OK;
+}
+
+// What a sampling call adds to the checks of its plain form, before anything is launched.
+static bi_status validate_sampling(const bi_model_config& c, const bi_sampling* s, int64_t B, const char* who) {
+  if (c.vocab > kMaxSampleVocab)
+    return fail(BI_ERR_UNSUPPORTED_SHAPE, std::string(who) + ": vocab must be at most " + std::to_string(kMaxSampleVocab));
+  if (s && (s->temperature || s->top_k || s->top_p || s->min_p) && s->n < B)
+    return fail(BI_ERR_INVALID_ARG, std::string(who) + ": fewer sampling parameters than sequences");
   return BI_OK;
 }
 
@@ -472,12 +509,20 @@ size_t bi_forward_workspace_size(const bi_model_config* cfg, int64_t max_tokens,
   return bi::plan_layout(*cfg, max_tokens, max_pieces, max_ctx, max_logit_rows, mode).total;
 }
 
-bi_status bi_forward_prefill(bi_model* m, const int32_t* tokens, const int32_t* target_ids, const int64_t* cu_seqlens,
-                             const int64_t* start_pos, const int64_t* logit_from, int64_t B, int64_t chunk,
-                             const int32_t* block_table, int64_t max_blocks_per_seq, void* k_cache, void* v_cache,
-                             int64_t n_blocks, float* logprob_out, int32_t* sampled_out, void* workspace,
-                             size_t ws_bytes, int64_t max_tokens, int64_t max_ctx, int64_t max_logit_rows, int mode,
-                             void* stream) {
+size_t bi_forward_sample_workspace_size(const bi_model_config* cfg, int64_t max_tokens, int64_t max_pieces,
+                                        int64_t max_ctx, int64_t max_logit_rows, int mode) {
+  if (!cfg || max_tokens <= 0 || max_pieces <= 0 || max_ctx <= 0 || max_logit_rows <= 0) return 0;
+  return bi::plan_layout(*cfg, max_tokens, max_pieces, max_ctx, max_logit_rows, mode, true).total;
+}
+
+// bi_forward_prefill, or with `sample` its sampling form.
+static bi_status forward_prefill(bi_model* m, const int32_t* tokens, const int32_t* target_ids,
+                                 const int64_t* cu_seqlens, const int64_t* start_pos, const int64_t* logit_from,
+                                 int64_t B, int64_t chunk, const int32_t* block_table, int64_t max_blocks_per_seq,
+                                 void* k_cache, void* v_cache, int64_t n_blocks, float* logprob_out,
+                                 int32_t* sampled_out, void* workspace, size_t ws_bytes, int64_t max_tokens,
+                                 int64_t max_ctx, int64_t max_logit_rows, int mode, void* stream,
+                                 const bi::SampleHead* sample) {
   using namespace bi;
   BI_REQUIRE(m && cu_seqlens && start_pos, "null model or metadata");
   BI_REQUIRE(B >= 0, "B < 0");
@@ -487,8 +532,11 @@ bi_status bi_forward_prefill(bi_model* m, const int32_t* tokens, const int32_t* 
   BI_REQUIRE(mode == BI_INVARIANT || mode == BI_FAST, "bad mode");
   const bi_model_config& c = m->cfg;
   const int64_t Pm = std::min<int64_t>(kMaxPiecesPerPass, std::max<int64_t>(B, 1));
-  const FwdLayout L = plan_layout(c, max_tokens, Pm, max_ctx, max_logit_rows, mode);
-  BI_REQUIRE(ws_bytes >= L.total, "forward workspace too small (bi_forward_workspace_size with max_pieces >= min(B, 128))");
+  const FwdLayout L = plan_layout(c, max_tokens, Pm, max_ctx, max_logit_rows, mode, sample != nullptr);
+  BI_REQUIRE(ws_bytes >= L.total, sample ? "forward workspace too small (bi_forward_sample_workspace_size with "
+                                           "max_pieces >= min(B, 128))"
+                                         : "forward workspace too small (bi_forward_workspace_size with max_pieces "
+                                           ">= min(B, 128))");
   BI_REQUIRE(cu_seqlens[0] == 0, "cu_seqlens[0] must be 0");
   for (int64_t b = 0; b < B; ++b) {
     BI_REQUIRE(cu_seqlens[b + 1] >= cu_seqlens[b], "cu_seqlens must be non-decreasing");
@@ -509,14 +557,44 @@ bi_status bi_forward_prefill(bi_model* m, const int32_t* tokens, const int32_t* 
                at<int32_t>(workspace, L.piece_pos0), at<int32_t>(workspace, L.ids),
                at<int32_t>(workspace, L.logit_src), at<int32_t>(workspace, L.logit_dst),
                at<int32_t>(workspace, L.logit_tgt), at<int32_t>(workspace, L.row_seq),
-               at<int32_t>(workspace, L.row_pos)};
+               at<int32_t>(workspace, L.row_pos), sample ? at<int32_t>(workspace, L.logit_seq) : nullptr};
     BI_TRY(launched(launch_pdl(pass_meta_kernel, dim3((unsigned)cdiv(std::max<int64_t>(rows, 1), 256)), dim3(256), 0,
                                st, pm, tokens, target_ids, dm),
                     "pass_meta_kernel"));
     BI_TRY(run_pass(m, workspace, L, ps, max_logit_rows, block_table, max_blocks_per_seq, k_cache, v_cache, n_blocks,
-                    target_ids == nullptr, logprob_out, sampled_out, mode, stream));
+                    target_ids == nullptr, logprob_out, sampled_out, mode, stream, sample));
   }
   return BI_OK;
+}
+
+bi_status bi_forward_prefill(bi_model* m, const int32_t* tokens, const int32_t* target_ids, const int64_t* cu_seqlens,
+                             const int64_t* start_pos, const int64_t* logit_from, int64_t B, int64_t chunk,
+                             const int32_t* block_table, int64_t max_blocks_per_seq, void* k_cache, void* v_cache,
+                             int64_t n_blocks, float* logprob_out, int32_t* sampled_out, void* workspace,
+                             size_t ws_bytes, int64_t max_tokens, int64_t max_ctx, int64_t max_logit_rows, int mode,
+                             void* stream) {
+  return forward_prefill(m, tokens, target_ids, cu_seqlens, start_pos, logit_from, B, chunk, block_table,
+                         max_blocks_per_seq, k_cache, v_cache, n_blocks, logprob_out, sampled_out, workspace, ws_bytes,
+                         max_tokens, max_ctx, max_logit_rows, mode, stream, nullptr);
+}
+
+bi_status bi_forward_prefill_sample(bi_model* m, const int32_t* tokens, const int32_t* target_ids,
+                                    const bi_sampling* sampling, const float* u, const int64_t* cu_seqlens,
+                                    const int64_t* start_pos, const int64_t* logit_from, int64_t B, int64_t chunk,
+                                    const int32_t* block_table, int64_t max_blocks_per_seq, void* k_cache,
+                                    void* v_cache, int64_t n_blocks, float* logprob_out, int32_t* sampled_out,
+                                    void* workspace, size_t ws_bytes, int64_t max_tokens, int64_t max_ctx,
+                                    int64_t max_logit_rows, int mode, void* stream) {
+  BI_REQUIRE(m && cu_seqlens, "null model or metadata");
+  BI_REQUIRE(B >= 0, "B < 0");
+  if (B == 0) return BI_OK;
+  BI_REQUIRE((target_ids != nullptr) != (u != nullptr), "either target_ids (score) or u (draw), not both");
+  BI_REQUIRE(!u || sampled_out, "a draw needs sampled_out");
+  BI_TRY(bi::validate_sampling(m->cfg, sampling, B, __func__));
+  const bi::SampleHead sh{sampling, u, cu_seqlens[B], 1, nullptr};
+  return forward_prefill(m, tokens, target_ids, cu_seqlens, start_pos, logit_from, B, chunk, block_table,
+                         max_blocks_per_seq, k_cache, v_cache, n_blocks, logprob_out, u ? sampled_out : nullptr,
+                         workspace, ws_bytes, max_tokens, max_ctx, max_logit_rows, mode, stream, &sh);
 }
 
 int64_t bi_prefill_plan(const int64_t* cu_seqlens, const int64_t* start_pos, const int64_t* logit_from, int64_t B,
@@ -546,10 +624,12 @@ int64_t bi_prefill_plan(const int64_t* cu_seqlens, const int64_t* start_pos, con
   return n;
 }
 
-bi_status bi_forward_decode(bi_model* m, const int32_t* tokens, const int32_t* pos, int64_t B,
-                            const int32_t* block_table, int64_t max_blocks_per_seq, void* k_cache, void* v_cache,
-                            int64_t n_blocks, int64_t max_ctx, int32_t* sampled_out, float* logprob_out,
-                            void* workspace, size_t ws_bytes, int mode, void* stream) {
+// bi_forward_decode, or with `sample` its sampling form.
+static bi_status forward_decode(bi_model* m, const int32_t* tokens, const int32_t* pos, int64_t B,
+                                const int32_t* block_table, int64_t max_blocks_per_seq, void* k_cache, void* v_cache,
+                                int64_t n_blocks, int64_t max_ctx, int32_t* sampled_out, float* logprob_out,
+                                void* workspace, size_t ws_bytes, int mode, void* stream,
+                                const bi::SampleHead* sample) {
   using namespace bi;
   BI_REQUIRE(m, "null model");
   BI_REQUIRE(B >= 0, "B < 0");
@@ -560,12 +640,15 @@ bi_status bi_forward_decode(bi_model* m, const int32_t* tokens, const int32_t* p
   BI_REQUIRE(cdiv(max_ctx, 64) <= max_blocks_per_seq, "block table shorter than max_ctx");
   BI_REQUIRE(B <= 65535, "B too large");
   BI_REQUIRE(mode == BI_INVARIANT || mode == BI_FAST, "bad mode");
-  const FwdLayout L = plan_layout(m->cfg, B, B, max_ctx, B, mode);
-  BI_REQUIRE(ws_bytes >= L.total, "forward workspace too small (bi_forward_workspace_size(cfg, B, B, max_ctx, B))");
+  const FwdLayout L = plan_layout(m->cfg, B, B, max_ctx, B, mode, sample != nullptr);
+  BI_REQUIRE(ws_bytes >= L.total,
+             sample ? "forward workspace too small (bi_forward_sample_workspace_size(cfg, B, B, max_ctx, B))"
+                    : "forward workspace too small (bi_forward_workspace_size(cfg, B, B, max_ctx, B))");
   DevMeta dm{at<int32_t>(workspace, L.piece_seq), at<int32_t>(workspace, L.piece_row0),
              at<int32_t>(workspace, L.piece_pos0), at<int32_t>(workspace, L.ids), at<int32_t>(workspace, L.logit_src),
              at<int32_t>(workspace, L.logit_dst), at<int32_t>(workspace, L.logit_tgt),
-             at<int32_t>(workspace, L.row_seq), at<int32_t>(workspace, L.row_pos)};
+             at<int32_t>(workspace, L.row_seq), at<int32_t>(workspace, L.row_pos),
+             sample ? at<int32_t>(workspace, L.logit_seq) : nullptr};
   const cudaStream_t st = as_stream(stream);
   BI_TRY(launched(launch_pdl(decode_embed_kernel, dim3((unsigned)B), dim3(128), 0, st, tokens, pos, (int)B, dm,
                              static_cast<const __nv_bfloat16*>(m->embed), m->cfg.vocab, m->cfg.d,
@@ -573,7 +656,30 @@ bi_status bi_forward_decode(bi_model* m, const int32_t* tokens, const int32_t* p
                   "decode_embed_kernel"));
   PassShape ps{B, B, 1, max_ctx, B, true};
   return run_pass(m, workspace, L, ps, B, block_table, max_blocks_per_seq, k_cache, v_cache, n_blocks, true,
-                  logprob_out, sampled_out, mode, stream);
+                  logprob_out, sampled_out, mode, stream, sample);
+}
+
+bi_status bi_forward_decode(bi_model* m, const int32_t* tokens, const int32_t* pos, int64_t B,
+                            const int32_t* block_table, int64_t max_blocks_per_seq, void* k_cache, void* v_cache,
+                            int64_t n_blocks, int64_t max_ctx, int32_t* sampled_out, float* logprob_out,
+                            void* workspace, size_t ws_bytes, int mode, void* stream) {
+  return forward_decode(m, tokens, pos, B, block_table, max_blocks_per_seq, k_cache, v_cache, n_blocks, max_ctx,
+                        sampled_out, logprob_out, workspace, ws_bytes, mode, stream, nullptr);
+}
+
+bi_status bi_forward_decode_sample(bi_model* m, const int32_t* tokens, const int32_t* pos, int64_t B,
+                                   const bi_sampling* sampling, const float* u, int64_t u_rows, const int32_t* u_row,
+                                   const int32_t* block_table, int64_t max_blocks_per_seq, void* k_cache,
+                                   void* v_cache, int64_t n_blocks, int64_t max_ctx, int32_t* sampled_out,
+                                   float* logprob_out, void* workspace, size_t ws_bytes, int mode, void* stream) {
+  BI_REQUIRE(m, "null model");
+  BI_REQUIRE(B >= 0, "B < 0");
+  if (B == 0) return BI_OK;
+  BI_REQUIRE(u && u_rows >= 1, "random numbers: u is NULL or u_rows < 1");
+  BI_TRY(bi::validate_sampling(m->cfg, sampling, B, __func__));
+  const bi::SampleHead sh{sampling, u, B, u_rows, u_row};
+  return forward_decode(m, tokens, pos, B, block_table, max_blocks_per_seq, k_cache, v_cache, n_blocks, max_ctx,
+                        sampled_out, logprob_out, workspace, ws_bytes, mode, stream, &sh);
 }
 
 }  // extern "C"

@@ -805,7 +805,7 @@ struct SmpRow {
 
   BI_DEV void write(int32_t id, float lp) {
     const int64_t o = a.dst ? (int64_t)a.dst[row] : row;
-    if (!SCORE) a.ids_out[o] = id;
+    if (!SCORE && a.ids_out) a.ids_out[o] = id;
     if (a.lp_out) a.lp_out[o] = lp;
   }
   BI_DEV float value(int32_t id) {
@@ -1090,6 +1090,7 @@ static bi_status sample_args(const char* who, const void* logits, int dtype, int
   if (!logits) return bad(BI_ERR_INVALID_ARG, "null logits");
   if (dtype != BI_DTYPE_FP32 && dtype != BI_DTYPE_BF16) return bad(BI_ERR_INVALID_ARG, "dtype must be BI_DTYPE_FP32 or BI_DTYPE_BF16");
   if (V < 1 || ld < V) return bad(BI_ERR_INVALID_ARG, "V must be positive and ld at least V");
+  static_assert(kSmpMaxV == kMaxSampleVocab, "vocabulary limit");
   if (V > kSmpMaxV) return bad(BI_ERR_UNSUPPORTED_SHAPE, "V must be at most 262144");
   if (T > 0x7fffffff / 8) return bad(BI_ERR_INVALID_ARG, "T too large");
   if (ld > (int64_t(1) << 40)) return bad(BI_ERR_INVALID_ARG, "ld too large");
@@ -1111,6 +1112,23 @@ static bi_status sample_args(const char* who, const void* logits, int dtype, int
   a->param_row = param_row;
   a->status = device_status_ptr();
   return BI_OK;
+}
+
+bi_status sample_rows(const float* logits, int64_t T, int64_t V, const bi_sampling* sampling, const int32_t* param_row,
+                      const float* u, int64_t u_ld, int64_t u_rows, const int32_t* u_row, const int32_t* ids_in,
+                      const int32_t* dst, int32_t* ids_out, float* lp_out, cudaStream_t st) {
+  if (T == 0) return BI_OK;
+  SampleArgs a{};
+  BI_TRY(sample_args(__func__, logits, BI_DTYPE_FP32, T, V, V, sampling, param_row, &a));
+  a.u = u;
+  a.u_ld = u_ld;
+  a.u_rows = u_rows;
+  a.u_row = u_row;
+  a.ids_in = ids_in;
+  a.dst = dst;
+  a.ids_out = ids_out;
+  a.lp_out = lp_out;
+  return ids_in ? dispatch_sample<float, true>(a, T, st) : dispatch_sample<float, false>(a, T, st);
 }
 
 }  // namespace bi

@@ -95,6 +95,24 @@ class KVCache:
     n_blocks: int
 
 
+class KVPool:
+    """Blocks of a paged cache handed out on the device as sequences grow (bi_block_table_resize).
+
+    `table` [n_seq, max_blocks] is the block table of the forward calls; the free ids stand in a ring."""
+
+    def __init__(self, n_seq: int, max_blocks: int, n_blocks: int, device="cuda", seed: int | None = None):
+        self.n_seq, self.max_blocks, self.n_blocks = n_seq, max_blocks, n_blocks
+        self.table = torch.full((n_seq, max_blocks), -1, dtype=torch.int32, device=device)
+        self.owned = torch.zeros(n_seq, dtype=torch.int32, device=device)
+        self.ring = torch.from_numpy(block_ids(1, n_blocks, seed)[0]).to(device)
+        self.pool = torch.tensor([0, n_blocks], dtype=torch.int32, device=device)
+
+    def resize(self, lens: torch.Tensor, extra: int = 0):
+        """Blocks for lens + extra tokens of every sequence (int32 on the device; 0: all given back)."""
+        L.bi_block_table_resize(lens, self.n_seq, self.table, self.max_blocks, self.owned, self.ring, self.n_blocks,
+                                self.pool, extra=extra)
+
+
 class Decoder:
     """A decoder whose weights live in caller-owned (torch) device memory."""
 
@@ -180,18 +198,22 @@ class Decoder:
         tab, total = paged_block_ids(ctx_lens, max_blocks, seed)
         return torch.from_numpy(tab).to(self.device), total
 
-    def workspace(self, max_tokens, max_pieces, max_ctx, max_logit_rows, mode=L.BI_INVARIANT) -> torch.Tensor:
-        n = L.bi_forward_workspace_size(self.cfg, max_tokens, max_pieces, max_ctx, max_logit_rows, mode)
+    def workspace(self, max_tokens, max_pieces, max_ctx, max_logit_rows, mode=L.BI_INVARIANT,
+                  sampling=False) -> torch.Tensor:
+        size = L.bi_forward_sample_workspace_size if sampling else L.bi_forward_workspace_size
+        n = size(self.cfg, max_tokens, max_pieces, max_ctx, max_logit_rows, mode)
         return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     # ------------------------------------------------------------ calls
     def prefill(self, seqs, cache: KVCache, block_table: torch.Tensor, start_pos=None, logit_from=None,
                 targets=None, chunk=2048, max_tokens=8192, max_ctx=None, max_logit_rows=2048,
-                mode=L.BI_INVARIANT, workspace=None, tokens_dev=None, dump=None):
+                mode=L.BI_INVARIANT, workspace=None, tokens_dev=None, dump=None, sampling=None, u=None):
         """Packed prefill of a list of token arrays; returns (logprob [T], sampled [T]) over the packed rows.
 
         `dump` (bf16 [n_layers + 2, rows, d]) receives the per-layer residual
-        stream of a single-pass call (see bi_model_set_dump)."""
+        stream of a single-pass call (see bi_model_set_dump).  With `sampling` (bi_sampling,
+        one entry per sequence) the targets are scored under it, or without targets tokens
+        are drawn with `u` (fp32 [T] on the device, one per packed row)."""
         lens = [len(x) for x in seqs]
         B = len(seqs)
         cu = np.zeros(B + 1, dtype=np.int64)
@@ -208,13 +230,19 @@ class Decoder:
         lp = torch.full((T,), float("nan"), dtype=torch.float32, device=self.device)
         sm = torch.full((T,), -1, dtype=torch.int32, device=self.device)
         if workspace is None:
-            workspace = self.workspace(max_tokens, min(B, 128), max_ctx, max_logit_rows, mode)
+            workspace = self.workspace(max_tokens, min(B, 128), max_ctx, max_logit_rows, mode, sampling is not None)
         if dump is not None:
             L.bi_model_set_dump(self.handle, dump, dump.shape[1])
         try:
-            L.bi_forward_prefill(self.handle, tokens_dev, tgt, cu, start_pos, logit_from, B, chunk, block_table,
-                                 block_table.shape[1], cache.k, cache.v, cache.n_blocks, lp, sm, workspace, max_tokens,
-                                 max_ctx, max_logit_rows, mode)
+            if sampling is not None:
+                L.bi_forward_prefill_sample(self.handle, tokens_dev, tgt, sampling, u, cu, start_pos, logit_from, B,
+                                            chunk, block_table, block_table.shape[1], cache.k, cache.v,
+                                            cache.n_blocks, lp, sm, workspace, max_tokens, max_ctx, max_logit_rows,
+                                            mode)
+            else:
+                L.bi_forward_prefill(self.handle, tokens_dev, tgt, cu, start_pos, logit_from, B, chunk, block_table,
+                                     block_table.shape[1], cache.k, cache.v, cache.n_blocks, lp, sm, workspace,
+                                     max_tokens, max_ctx, max_logit_rows, mode)
         finally:
             if dump is not None:
                 L.bi_model_set_dump(self.handle, None, 0)
@@ -227,28 +255,53 @@ class Decoder:
 
     # ------------------------------------------------------------ RL halves
     def rollout(self, prompts, n_gen: int, cache: KVCache, block_table: torch.Tensor, chunk=2048, use_graph=True,
-                mode=L.BI_INVARIANT, prefill_max_tokens=8192):
-        """Greedy rollout: prefill, then n_gen - 1 decode steps.  Returns (ids [B, n_gen], lp [B, n_gen]) on device."""
+                mode=L.BI_INVARIANT, prefill_max_tokens=8192, sampling=None, uniforms=None, pool: KVPool | None = None):
+        """Rollout: prefill, then n_gen - 1 decode steps.  Returns (ids [B, n_gen], lp [B, n_gen]) on device.
+
+        Greedy, or with `sampling` (bi_sampling, one entry per sequence) drawn with
+        `uniforms` (fp32 [n_gen, B] on the device, in [0, 1)): token j of sequence b
+        with uniforms[j, b].  With `pool` the block table is the pool's (`block_table`
+        is not used) and every step takes the blocks it grows into."""
         B = len(prompts)
+        if (sampling is None) != (uniforms is None):
+            raise ValueError("sampling and uniforms go together")
+        if uniforms is not None and (tuple(uniforms.shape) != (n_gen, B) or uniforms.dtype != torch.float32
+                                     or not uniforms.is_contiguous()):
+            raise ValueError(f"uniforms must be contiguous fp32 [{n_gen}, {B}]")
         lens = np.array([len(p) for p in prompts])
         max_ctx = int(lens.max()) + n_gen
         dev = self.device
+        last = torch.from_numpy(np.cumsum(lens) - 1).to(dev)
+        pos = torch.from_numpy(lens.astype(np.int32)).to(dev)
+        if pool is not None:
+            block_table = pool.table
+            pool.resize(pos)
+        u0 = None
+        if sampling is not None:
+            u0 = torch.zeros(int(lens.sum()), dtype=torch.float32, device=dev)
+            u0[last] = uniforms[0]
         lp0, sm0, cu = self.prefill(prompts, cache, block_table, logit_from=[n - 1 for n in lens], chunk=chunk,
-                                    max_tokens=prefill_max_tokens, max_ctx=max_ctx, mode=mode)
-        last = torch.from_numpy(cu[1:] - 1).to(dev)
+                                    max_tokens=prefill_max_tokens, max_ctx=max_ctx, mode=mode, sampling=sampling,
+                                    u=u0)
         hist_ids = torch.zeros((n_gen, B), dtype=torch.int32, device=dev)
         hist_lp = torch.zeros((n_gen, B), dtype=torch.float32, device=dev)
         hist_ids[0] = sm0[last]
         hist_lp[0] = lp0[last]
         tok = hist_ids[0].clone()
-        pos = torch.from_numpy(lens.astype(np.int32)).to(dev)
         step = torch.ones(1, dtype=torch.int32, device=dev)
         sampled = torch.zeros(B, dtype=torch.int32, device=dev)
         lp = torch.zeros(B, dtype=torch.float32, device=dev)
-        ws = self.workspace(B, B, max_ctx, B, mode)
+        ws = self.workspace(B, B, max_ctx, B, mode, sampling is not None)
 
         def one_step():
-            self.decode(tok, pos, cache, block_table, max_ctx, sampled, lp, ws, mode)
+            if pool is not None:
+                pool.resize(pos, extra=1)
+            if sampling is not None:
+                L.bi_forward_decode_sample(self.handle, tok, pos, B, sampling, uniforms, block_table,
+                                           block_table.shape[1], cache.k, cache.v, cache.n_blocks, max_ctx, sampled,
+                                           lp, ws, u_rows=n_gen, u_row=step, mode=mode)
+            else:
+                self.decode(tok, pos, cache, block_table, max_ctx, sampled, lp, ws, mode)
             L.bi_decode_advance(sampled, lp, tok, pos, B, step, hist_ids, hist_lp, n_gen)
 
         n_steps = n_gen - 1
@@ -267,17 +320,21 @@ class Decoder:
         return hist_ids.T.contiguous(), hist_lp.T.contiguous()
 
     def recompute(self, prompts, gens, cache: KVCache, block_table: torch.Tensor, chunk=2048, order=None,
-                  mode=L.BI_INVARIANT, max_tokens=8192, max_logit_rows=2048):
+                  mode=L.BI_INVARIANT, max_tokens=8192, max_logit_rows=2048, sampling=None):
         """Training-side scoring of prompt + response; returns lp [B, n_gen] (device).
 
-        `order` packs the sequences in another order (a different batch layout)."""
+        `order` packs the sequences in another order (a different batch layout).  `sampling`:
+        the rollout's parameters; the logprobs are then those of its truncated distributions."""
         B = len(prompts)
         order = list(range(B)) if order is None else list(order)
         gens = [np.asarray(g, np.int32) for g in gens]
         seqs, tg, lf = recompute_pack(prompts, gens, order)
         bt = block_table[torch.as_tensor(order, device=block_table.device)]
+        if sampling is not None:
+            idx = torch.as_tensor(order, device=self.device)
+            sampling = L.bi_sampling(*(None if t is None else t[idx] for t in sampling.tensors))
         lp, _, cu = self.prefill(seqs, cache, bt, logit_from=lf, targets=tg, chunk=chunk, max_tokens=max_tokens,
-                                 max_logit_rows=max_logit_rows, mode=mode)
+                                 max_logit_rows=max_logit_rows, mode=mode, sampling=sampling)
         out = torch.empty((B, len(gens[0])), dtype=torch.float32, device=self.device)
         for j, b in enumerate(order):
             out[b] = lp[int(cu[j]) + lf[j]: int(cu[j + 1])]
