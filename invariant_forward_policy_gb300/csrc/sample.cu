@@ -19,17 +19,20 @@
 // them alone, and so a row's bits depend neither on how many CTAs share it, nor on which of the
 // ways to its cut below was taken, nor on T.
 //
-// A row is read once, into the shared memory of a cluster of 1, 2, 4 or 8 CTAs (fp32).  Then
+// A row is shared by a cluster of 1, 2, 4 or 8 CTAs, each with a contiguous share that its passes stream
+// (the first from HBM, the others from L2).  The first pass finds the maximum.  Then
 //  - nothing cut but by min-p: one pass sums the masses;
-//  - top_k up to 1024: the k-th largest of the threads' own maxima (known from the read) bounds the
-//    k-th largest logit from below, so that only a few more than k logits pass it; one CTA orders
-//    those and does the rest;
-//  - top-p: a histogram of counts over k = 64 log2 w (1/64 octave) predicts where the cut is; one
+//  - top_k up to 1024: in each CTA the k'-th largest of the threads' own maxima (known from the read),
+//    k' somewhat above the CTA's share of k, lets through somewhat more than k' logits; one CTA orders
+//    what the CTAs let through and does the rest, provided that the k-th of them is not below any
+//    CTA's bound;
+//  - top-p: a histogram of counts over k = 64 log2 w (1/32 octave) predicts where the cut is; one
 //    pass sums the masses and lists the logits next to the prediction, and one CTA orders the list
 //    and finds the cut, exactly;
-//  - anything else (top_k above 1024, lists that overflow, a missed prediction): the cut by
-//    histograms with masses, on octaves first and on the float's bits then, until the bin fits the
-//    sort or holds equal values only, whose first few by index are counted out.
+//  - anything else (larger top_k, rows of logits beyond 2^13 octaves, a list that overflows, a missed
+//    prediction): one CTA finds the cut from global memory by histograms with masses, on octaves first and
+//    on the float's bits then, until the bin fits the sort or holds equal values only, whose first few
+//    by index are counted out.
 // The draw finds the CTA, then the warp, then the token whose running mass crosses u S.
 #include <cooperative_groups.h>
 
@@ -49,22 +52,24 @@ typedef unsigned long long u64;
 
 constexpr int kSmpThreads = 512;
 constexpr int kSmpWarps = kSmpThreads / 32;
-constexpr int kSmpBins = 2048;             // bins of top-p's counts; the last one is open
+constexpr int kSmpBins = 1024;             // bins of top-p's counts (1/32 octave); the last one is open
 constexpr int kSmpMaxBins = 256;           // bins of the threads' maxima
-constexpr int kSmpMassBins = 1024;         // bins of a histogram with masses (count and three 16-bit limbs)
+constexpr int kSmpMassBins = kSmpThreads;          // bins of a histogram with masses (count and four 12-bit limbs)
+constexpr int kSmpMassShift = 2;           // 32 octaves of 1/64 over them
+constexpr int kSmpMassBits = 9;            // log2 of them
 constexpr int kSmpList = 2048;             // candidates that one CTA orders
-constexpr int kSmpLocal = 1024;            // candidates that one CTA of several lists
 constexpr int kSmpMaxK = 1024;             // top_k up to which the kept set goes straight to the list
-constexpr int kSmpMaxShare = 32768;        // logits of one CTA: a limb's sum stays below 2^31
-constexpr int kSmpMaxV = 8 * kSmpMaxShare; // 2^18 masses below 2^44.6 sum to less than 2^63
-constexpr int kSmpOne = 380000000;         // mantissa of 1: the largest for which the table's products below round
-                                           // by the magic number (|2 kSmpOne (2^(1/128) - 1)| < 2^22), with some room
+constexpr int kSmpMaxShareK = kSmpThreads * 3 / 4;        // and each CTA's bound is the k'-th maximum for k' up to this
+constexpr int kSmpMaxV = 1 << 18;          // 2^18 masses below 2^44.6 sum to less than 2^63
+// The table's mantissa of 1 is 380000000: about the largest for which its products with 2^(f/64) - 1 round
+// by the magic number (2 * 380000000 * (2^(1/128) - 1) is below 2^22).
 constexpr int kSmpFrac = 15;               // mass = mantissa (below 2^29.6) << 15 >> octaves below the largest
 constexpr int kSmpTabLanes = 16;           // table copies: 8-byte reads of a half-warp have no bank conflict
+constexpr int kSmpSmem = 64 * kSmpTabLanes * 8 + 8192 + kSmpList * 8;  // table, counts, list
 constexpr float kSmpMagic = 12582912.f;    // 1.5 * 2^23: adding it rounds to an integer in the low bits
 constexpr int kSmpMagicBits = 0x4B400000;
 
-// round(kSmpOne * 2^(j / 64))
+// round(380000000 * 2^(j / 64))
 __constant__ uint32_t kExp2Tab[64] = {
     380000000, 384137929, 388320916, 392549454, 396824037, 401145168, 405513352, 409929103,
     414392938, 418905382, 423466962, 428078215, 432739681, 437451907, 442215446, 447030857,
@@ -100,8 +105,8 @@ struct SmpCut {  // an element is kept iff its key is larger, or equal and its i
   int32_t idx;   // -1: no cut was found
   u64 mass;      // mass through the cut
 };
-struct SmpFind { // a bin and what lies before it
-  int32_t bin;   // -1: the target is beyond the total
+struct SmpFind { // a bin and what lies before it and in it
+  int32_t bin;
   uint32_t before, inside;
   u64 before_mass, inside_mass;
 };
@@ -111,23 +116,23 @@ struct SmpShared {
   // the row's parameters, by one thread
   double log_min_p;               // T ln(min_p)
   float c_hi, c_lo, r_hi, r_lo;   // 64 log2(e) / T and 1 / T, each in two floats
+  float floor_abs, floor_rel;     // the mass functions' lowest arguments
   float p, u, min_p, x_id;
   int32_t k_eff, id, ok;
+  // the warps' values
   float wmax[kSmpWarps], wmin[kSmpWarps];
-  // written by the cluster's CTAs, each at its rank: what all of them need is then at hand locally
-  float cta_max[8], cta_min[8];
-  u64 cta_sum[8];
-  int32_t cta_idx[8];
-  // values that the cluster's other CTAs read, or write here
   u64 wsum[kSmpWarps], wsum2[kSmpWarps];
   uint32_t wcnt[kSmpWarps];
-  u64 pub_sum[2];                 // two sets, used in turn
-  uint32_t pub_cnt[2], pub_lo[2], pub_hi[2];
-  uint32_t list_n;                // entries of this CTA's own list (rank 0: of the joint list)
-  SmpFind find;
+  // written by the cluster's CTAs, each at its rank: what is needed of all of them is then at hand locally
+  float cta_max[8], cta_min[8], cta_bound[8];
+  u64 cta_sum[8], cta_sum2[8];
+  uint32_t cta_n[8];
+  float x_lo, x_hi;               // top-p's prediction
   SmpCut cut;
-  // one CTA's results
+  // this CTA's own
+  uint32_t list_n;
   float x_cut;
+  SmpFind find;
   u64 total, total2;
   int32_t pos;
 };
@@ -212,15 +217,15 @@ struct SmpMass {
   // 2^(f/64) - 1: the series to the third power of f ln2 / 64 (below 0.0055; the next term is 4e-11)
   static constexpr float a1 = 0.0108304247f, a2 = 5.86490496e-05f, a3 = 2.11731372e-07f;
   float m, c_hi, c_lo;
-  float floor_;  // ABS: logits below it are raised to it; else: x - m at or below it has no mass
+  float floor_;  // ABS: logits below it are raised to it (-2^20 / c); else: x - m at or below it has no mass (-4096 / c)
   int k_top;     // k of the maximum
   int oct_top;   // its octave
   int shift0;    // (shift0 - bits of the rounded sum) >> 6 = 32 - kSmpFrac + octaves below the top one
-  BI_DEV void init(float m_, float hi, float lo) {
+  BI_DEV void init(float m_, const SmpShared& sh) {
     m = m_;
-    c_hi = hi;
-    c_lo = lo;
-    floor_ = __fdiv_rn(ABS ? -1048576.f : -4096.f, c_hi);
+    c_hi = sh.c_hi;
+    c_lo = sh.c_lo;
+    floor_ = ABS ? sh.floor_abs : sh.floor_rel;
     k_top = ABS ? k_of(m) : 0;
     oct_top = k_top >> 6;
     shift0 = (oct_top + 32 - kSmpFrac) * 64 + 63 + kSmpMagicBits;
@@ -230,16 +235,18 @@ struct SmpMass {
     if (ABS) return __float_as_int(__fmaf_rn(fmaxf(x, floor_), c_hi, kSmpMagic)) - kSmpMagicBits;
     return __float_as_int(__fmaf_rn(fmaxf(__fsub_rn(x, m), floor_), c_hi, kSmpMagic)) - kSmpMagicBits;
   }
-  BI_DEV int bin(float x) const { return min(k_top - k_of(x), kSmpBins - 1); }
   // The mass from the rounded sum (k in its low bits) and g = 2^(f/64) - 1: the table's 2^(k mod 64 / 64) and its
   // product with g, rounded to an integer by the magic number (taken off the table's integers), then shifted by
-  // the octave: (mantissa 2^32) >> s, where a shift of 64 or more gives 0.
+  // the octave: (mantissa 2^32) >> s, where a shift of 64 or more gives 0.  The last bit is set in place of what the
+  // shift drops, which leaves no bias: many small masses, each cut by half a unit on average, would move the running
+  // sum by more than one of them.
   BI_DEV u64 scale(int q, float g, const uint2* tab) const {
     const uint2 t = tab[(q & 63) * kSmpTabLanes];
     const uint32_t M = t.x + (uint32_t)__float_as_int(__fmaf_rn(__uint_as_float(t.y), g, kSmpMagic));
     u64 w;
-    asm("shr.b64 %0, %1, %2;" : "=l"(w) : "l"((u64)M << 32), "r"((shift0 - q) >> 6));
-    return w;
+    const uint32_t by = (uint32_t)((shift0 - q) >> 6);
+    asm("shr.b64 %0, %1, %2;" : "=l"(w) : "l"((u64)M << 32), "r"(by));
+    return by < 64u ? w | 1ull : 0ull;
   }
   BI_DEV u64 mass(float x, const uint2* tab) const {
     float q, f;
@@ -288,6 +295,14 @@ struct SmpMass {
   }
 };
 
+// v = (h + l) 2^e to 48 bits: h 24 bits in [2^23, 2^24), l the next 24
+BI_DEV void smp_split(u64 v, float& h, float& l, int& e) {
+  const int z = __clzll((long long)v);
+  const u64 n = v << z;
+  h = (float)(uint32_t)(n >> 40);
+  l = __fmul_rn((float)((uint32_t)(n >> 16) & 0xffffffu), 0x1p-24f);
+  e = 40 - z;
+}
 // ln of a kept token's probability: (x - m) / T - ln(S / W), W the mass of the maximum; both terms in two
 // floats until the last sum.
 BI_DEV float smp_logprob(float x, float m, float r_hi, float r_lo, u64 S, u64 W) {
@@ -295,457 +310,344 @@ BI_DEV float smp_logprob(float x, float m, float r_hi, float r_lo, u64 S, u64 W)
   const float d = smp_diff(x, m, &dl);
   const float ah = __fmul_rn(d, r_hi);
   const float al = __fadd_rn(__fmaf_rn(d, r_hi, -ah), __fmaf_rn(d, r_lo, __fmul_rn(dl, r_hi)));
-  // q = S / W in two floats, S and W each split into 24 and 40 bits
-  const float sh = __ull2float_rz(S & ~0xffffffffffull), sl = __ull2float_rn(S & 0xffffffffffull);
-  const float wh = __ull2float_rz(W & ~0xffffffull), wl = __ull2float_rn(W & 0xffffffull);  // W < 2^45
-  float qh = __fdiv_rn(__fadd_rn(sh, sl), __fadd_rn(wh, wl));
-  const float rem = __fadd_rn(__fmaf_rn(-qh, wh, sh), __fmaf_rn(-qh, wl, sl));
-  float ql = __fdiv_rn(rem, wh);
-  // S may exceed 2^40 sums of 24 bits: sh holds 23 bits above bit 40, exact
-  int e = (__float_as_int(qh) >> 23) - 127;
-  const float scale = __int_as_float((127 - e) << 23);
-  qh = __fmul_rn(qh, scale);  // in [1, 2)
-  ql = __fmul_rn(ql, scale);
-  if (qh >= 1.5f) {
-    qh = __fmul_rn(qh, 0.5f);
-    ql = __fmul_rn(ql, 0.5f);
-    ++e;
+  float sh, sl, wh, wl;
+  int es, ew;
+  smp_split(S, sh, sl, es);
+  smp_split(W, wh, wl, ew);
+  // S / W = (qh + ql) 2^e with qh in [0.75, 1.5)
+  float qh = __fdiv_rn(sh, wh);  // in (1/2, 2)
+  float ql = __fdiv_rn(__fadd_rn(__fmaf_rn(-qh, wh, sh), __fmaf_rn(-qh, wl, sl)), wh);
+  int e = es - ew;
+  if (qh >= 1.5f || qh < 0.75f) {
+    const float by = qh >= 1.5f ? 0.5f : 2.f;
+    e += qh >= 1.5f ? 1 : -1;
+    qh = __fmul_rn(qh, by);
+    ql = __fmul_rn(ql, by);
   }
   const float ln2h = 45426.f / 65536.f, ln2l = 1.4286068203e-6f;  // e * ln2h is exact
   const float s = __fsub_rn(__fmaf_rn(-(float)e, ln2h, ah), logf(qh));
   return __fadd_rn(s, __fsub_rn(__fsub_rn(al, __fmul_rn((float)e, ln2l)), __fdiv_rn(ql, qh)));
 }
 
-// One row per cluster of CS CTAs.
-template <int CS>
-struct SmpRow {
+// ln of the probability of token (i, x) and the write of a row's results, by one thread.
+struct SmpOut {
   const SampleArgs& a;
-  SmpShared& sh;
-  float* xs;         // this CTA's logits, -inf before and after them
-  uint2* table;      // [64][kSmpTabLanes]
-  const uint2* tab;  // this lane's copy of it
-  unsigned char* area;  // 24 KB: own list or counts [kSmpBins] (8 KB); list or masses [4][kSmpMassBins] (16 KB)
-  cg::cluster_group cl;
-  int tid, warp, lane, rank;
-  int base;          // row index of position 0 of xs
-  int slabs, per;    // slabs of 128 positions of this CTA, and of each of its warps
-  int par;           // set of the published values in use
-  float m, x_min;    // row maximum; smallest logit that min-p keeps (above -inf)
   int64_t row;
-  int k_eff;
-  float p;
-  bool score;
-
-  BI_DEV uint32_t* counts() { return reinterpret_cast<uint32_t*>(area); }
-  BI_DEV u64* own_list() { return reinterpret_cast<u64*>(area); }
-  BI_DEV u64* list() { return reinterpret_cast<u64*>(area + kSmpLocal * 8); }
-
-  BI_DEV void csync() {
-    if (CS == 1) __syncthreads();
-    else cl.sync();
-  }
-  template <typename P>
-  BI_DEV P* at(P* ptr, int r) {
-    if (CS == 1) return ptr;
-    return cl.map_shared_rank(ptr, r);
-  }
-  BI_DEV int slab_lo(int w) { return min(slabs, w * per); }
-  BI_DEV int slab_hi(int w) { return min(slabs, w * per + per); }
-
-  // visit(position, x) for this warp's elements
-  template <typename F>
-  BI_DEV void each(F visit) {
-    const int s1 = slab_hi(warp);
-    for (int s = slab_lo(warp); s < s1; ++s) {
-      const int p0 = s * 128 + lane * 4;
-      const float4 v = *reinterpret_cast<const float4*>(xs + p0);
-      visit(p0, v.x);
-      visit(p0 + 1, v.y);
-      visit(p0 + 2, v.z);
-      visit(p0 + 3, v.w);
-    }
-  }
-
-  // Inclusive sums over the CTA's threads, and their totals.
-  BI_DEV void block_scan(uint32_t& c, u64& w, uint32_t* tot_c, u64* tot_w) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t c2 = __shfl_up_sync(0xffffffffu, c, o);
-      const u64 w2 = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) {
-        c += c2;
-        w += w2;
-      }
-    }
-    __syncthreads();
-    if (lane == 31) {
-      sh.wcnt[warp] = c;
-      sh.wsum[warp] = w;
-    }
-    __syncthreads();
-    uint32_t bc = 0, tc = 0;
-    u64 bw = 0, tw = 0;
-#pragma unroll
-    for (int i = 0; i < kSmpWarps; ++i) {
-      const uint32_t ci = sh.wcnt[i];
-      const u64 wi = sh.wsum[i];
-      if (i < warp) {
-        bc += ci;
-        bw += wi;
-      }
-      tc += ci;
-      tw += wi;
-    }
-    c += bc;
-    w += bw;
-    *tot_c = tc;
-    *tot_w = tw;
-  }
-  // Publishes this CTA's (count, mass); sums over lower ranks and over all ranks.
-  uint32_t base_c, tot_c;
-  u64 base_w, tot_w;
-  BI_DEV void cluster_scan(uint32_t c, u64 w) {
-    par ^= 1;
-    if (tid == 0) {
-      sh.pub_cnt[par] = c;
-      sh.pub_sum[par] = w;
-    }
-    csync();
-    base_c = tot_c = 0;
-    base_w = tot_w = 0;
-#pragma unroll
-    for (int r = 0; r < CS; ++r) {
-      const uint32_t cr = *at(&sh.pub_cnt[par], r);
-      const u64 wr = *at(&sh.pub_sum[par], r);
-      if (r < rank) {
-        base_c += cr;
-        base_w += wr;
-      }
-      tot_c += cr;
-      tot_w += wr;
-    }
-  }
-  // Rank r sums bins [r slice, (r + 1) slice) over the cluster (sum(b, &count, &mass)) and leaves their
-  // inclusive prefix sums in its own shared memory (put); base_* and tot_* then hold the ranks' sums.
-  template <int NB, typename F, typename G>
-  BI_DEV void reduce(F sum, G put) {
-    constexpr int slice = NB / CS;
-    constexpr int BPT = slice > kSmpThreads ? slice / kSmpThreads : 1;
-    uint32_t c[BPT], cs = 0;
-    u64 w[BPT], ws = 0;
-    const bool mine = tid * BPT < slice;
-#pragma unroll
-    for (int i = 0; i < BPT; ++i) {
-      c[i] = 0;
-      w[i] = 0;
-      if (mine) sum(rank * slice + tid * BPT + i, c[i], w[i]);
-      cs += c[i];
-      ws += w[i];
-      c[i] = cs;
-      w[i] = ws;
-    }
-    uint32_t ic = cs, tc;
-    u64 iw = ws, tw;
-    block_scan(ic, iw, &tc, &tw);
-    if (mine) {
-#pragma unroll
-      for (int i = 0; i < BPT; ++i) put(rank * slice + tid * BPT + i, ic - cs + c[i], iw - ws + w[i]);
-    }
-    cluster_scan(tc, tw);
-  }
-  // The bin where the running count or mass reaches target (>= 1), to every rank: get(b, &count, &mass) reads
-  // the prefix sums of reduce.
-  template <int NB, typename G>
-  BI_DEV SmpFind find(bool by_mass, u64 target, G get) {
-    constexpr int slice = NB / CS;
-    for (int i = tid; i < slice; i += kSmpThreads) {
-      const int b = rank * slice + i;
-      uint32_t c0 = base_c, c1;
-      u64 w0 = base_w, w1;
-      if (i > 0) {
-        get(b - 1, c1, w1);
-        c0 += c1;
-        w0 += w1;
-      }
-      get(b, c1, w1);
-      c1 += base_c;
-      w1 += base_w;
-      if (by_mass ? (w0 < target && target <= w1) : (c0 < target && target <= c1)) {
-        const SmpFind f{b, c0, c1 - c0, w0, w1 - w0};
-        for (int r = 0; r < CS; ++r) *at(&sh.find, r) = f;
-      }
-    }
-    csync();
-    return (by_mass ? tot_w : (u64)tot_c) < target ? SmpFind{-1, 0, 0, 0ull, 0ull} : sh.find;
-  }
-
-  // ---- lists of candidates: (key descending, index ascending) as one ascending 64-bit key
-  BI_DEV u64 entry(float x, int pos) { return (u64)(~smp_key(x)) << 32 | (uint32_t)(base + pos); }
-  BI_DEV static float entry_x(u64 e) { return smp_unkey(~(uint32_t)(e >> 32)); }
-  // Appends (warp-converged) to a list of at most cap entries; those beyond are counted only.
-  BI_DEV void append(bool take, float x, int pos, uint32_t* n, u64* l, uint32_t cap) {
-    const unsigned who = __ballot_sync(0xffffffffu, take);
-    if (who == 0u) return;
-    uint32_t o = 0;
-    if (lane == 0) o = atomicAdd(n, (uint32_t)__popc(who));
-    o = __shfl_sync(0xffffffffu, o, 0) + __popc(who & ((1u << lane) - 1u));
-    if (take && o < cap) l[o] = entry(x, pos);
-  }
-  // Bitonic sort of list[0, n) ascending (one CTA).
-  BI_DEV void sort(int n) {
-    u64* l = list();
-    int n2 = 2;
-    while (n2 < n) n2 <<= 1;
-    for (int i = n + tid; i < n2; i += kSmpThreads) l[i] = ~0ull;
-    __syncthreads();
-    for (int size = 2; size <= n2; size <<= 1)
-      for (int stride = size >> 1; stride > 0; stride >>= 1) {
-        for (int t = tid; t < n2 / 2; t += kSmpThreads) {
-          const int i = 2 * t - (t & (stride - 1)), j = i + stride;
-          const u64 x = l[i], y = l[j];
-          if ((x > y) == ((i & size) == 0)) {
-            l[i] = y;
-            l[j] = x;
-          }
-        }
-        __syncthreads();
-      }
-  }
-  // Masses of list[0, n) in order (mass_of(entry)), then the first entry at which the running mass (or, for
-  // !by_mass, the number of entries) reaches target_of(total mass): its position (n: none) and the mass through
-  // it, to every thread of the CTA.
-  template <typename F, typename G>
-  BI_DEV int list_find(int n, bool by_mass, F mass_of, G target_of, u64* through) {
-    constexpr int EPT = kSmpList / kSmpThreads;
-    const u64* l = list();
-    u64 w[EPT], ws = 0;
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const int e = tid * EPT + i;
-      w[i] = e < n ? mass_of(l[e]) : 0ull;
-      ws += w[i];
-    }
-    uint32_t c = 0, tc;
-    u64 run = ws, total;
-    if (tid == 0) sh.pos = n;
-    block_scan(c, run, &tc, &total);
-    run -= ws;
-    const u64 target = target_of(total);
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const int e = tid * EPT + i;
-      const u64 next = run + w[i];
-      if (e < n && (by_mass ? (run < target && target <= next) : (u64)(e + 1) == target)) {
-        sh.pos = e;
-        sh.total = next;
-      }
-      run = next;
-    }
-    __syncthreads();
-    const int pos = sh.pos;
-    *through = pos == n ? total : sh.total;
-    __syncthreads();
-    return pos;
-  }
-
-  // ceil(p S), at least 1: the mass at which top-p stops
-  BI_DEV u64 top_p_target(u64 S) {
-    if (!(p > 0.f)) return 1ull;
-    bool rest;
-    const u64 q = smp_mul_floor(p, S, &rest);
-    return q + (rest || q == 0ull ? 1ull : 0ull);
-  }
-  BI_DEV u64 draw_target(u64 S) {
-    bool rest;
-    return smp_mul_floor(sh.u, S, &rest) + 1ull;
-  }
-
-
-  BI_DEV void write(int32_t out_id, float lp) {
+  BI_DEV void write(int32_t id, float lp) const {
     const int64_t o = a.dst ? (int64_t)a.dst[row] : row;
-    if (!score && a.ids_out) a.ids_out[o] = out_id;
+    if (!a.ids_in && a.ids_out) a.ids_out[o] = id;
     if (a.lp_out) a.lp_out[o] = lp;
   }
   template <bool ABS>
-  BI_DEV void write_token(const SmpMass<ABS>& ms, int32_t i, float x, u64 S) {
-    write(i, smp_logprob(x, m, sh.r_hi, sh.r_lo, S, ms.mass(m, tab)));
+  BI_DEV void token(const SmpMass<ABS>& ms, const SmpShared& sh, const uint2* tab, int32_t id, float x, u64 S) const {
+    write(id, smp_logprob(x, ms.m, sh.r_hi, sh.r_lo, S, ms.mass(ms.m, tab)));
   }
-  BI_DEV float value(int32_t i) {
-    const int64_t at = row * a.ld + i;
-    return a.bf16 ? bf2f(static_cast<const __nv_bfloat16*>(a.logits)[at]) : static_cast<const float*>(a.logits)[at];
-  }
+};
 
-  // ---- sums over the row, and the draw.  weight4(index of the first, x, w) gives four elements' weights.
-  // Warp sums to sh.wsum; then, with publish(), the CTA's sum to every rank's sh.cta_sum.
+// ceil(p S), at least 1: the mass at which top-p stops
+BI_DEV u64 smp_top_p_target(float p, u64 S) {
+  if (!(p > 0.f)) return 1ull;
+  bool rest;
+  const u64 q = smp_mul_floor(p, S, &rest);
+  return q + (rest || q == 0ull ? 1ull : 0ull);
+}
+// floor(u S) + 1: the running mass that the drawn token is the first to reach
+BI_DEV u64 smp_draw_target(float u, u64 S) {
+  bool rest;
+  return smp_mul_floor(u, S, &rest) + 1ull;
+}
+// candidates: (key descending, index ascending) as one ascending 64-bit key
+BI_DEV u64 smp_entry(float x, int32_t i) { return (u64)(~smp_key(x)) << 32 | (uint32_t)i; }
+BI_DEV float smp_entry_x(u64 e) { return smp_unkey(~(uint32_t)(e >> 32)); }
+
+// ---------------------------------------------------------------- one CTA's helpers
+// Inclusive sum over the CTA's threads; *total: all of it.  wsum: a value per warp.
+BI_DEV u64 smp_block_scan(u64 w, u64* wsum, u64* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  __syncthreads();
+  if (lane == 31) wsum[warp] = w;
+  __syncthreads();
+  u64 before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kSmpWarps; ++i) {
+    const u64 t = wsum[i];
+    if (i < warp) before += t;
+    all += t;
+  }
+  *total = all;
+  return w + before;
+}
+// Sorts one value per thread, thread 0 the smallest: a bitonic network over the first n2 threads (a power of
+// two, uniform; the others' values must be ~0).  Strides within a warp exchange by shuffles, wider ones through
+// buf[kSmpThreads].
+BI_DEV u64 smp_sort_threads(u64 v, int n2, u64* buf) {
+  const int tid = threadIdx.x;
+  for (int size = 2; size <= n2; size <<= 1) {
+    for (int stride = size >> 1; stride > 0; stride >>= 1) {
+      u64 y;
+      if (stride >= 32) {
+        __syncthreads();
+        buf[tid] = v;
+        __syncthreads();
+        y = buf[tid ^ stride];
+      } else {
+        y = __shfl_xor_sync(0xffffffffu, v, stride);
+      }
+      const bool up = ((tid & size) == 0) == ((tid & stride) == 0);  // this thread keeps the smaller
+      v = (v < y) == up ? v : y;
+    }
+  }
+  return v;
+}
+// Sorts l[0, n) ascending, n <= kSmpList.
+BI_DEV void smp_sort(u64* l, int n) {
+  int n2 = 2;
+  while (n2 < n) n2 <<= 1;
+  for (int i = n + threadIdx.x; i < n2; i += kSmpThreads) l[i] = ~0ull;
+  __syncthreads();
+  for (int size = 2; size <= n2; size <<= 1)
+    for (int stride = size >> 1; stride > 0; stride >>= 1) {
+      for (int t = threadIdx.x; t < n2 / 2; t += kSmpThreads) {
+        const int i = 2 * t - (t & (stride - 1)), j = i + stride;
+        const u64 x = l[i], y = l[j];
+        if ((x > y) == ((i & size) == 0)) {
+          l[i] = y;
+          l[j] = x;
+        }
+      }
+      __syncthreads();
+    }
+}
+// Masses of l[0, n) in order (mass_of(entry)), then the first entry at which the running mass (or, for !by_mass,
+// the number of entries) reaches target_of(total mass): its position (n: none) and the mass through it, to every
+// thread.
+template <typename F, typename G>
+BI_DEV int smp_list_find(SmpShared& sh, const u64* l, int n, bool by_mass, F mass_of, G target_of, u64* through) {
+  constexpr int EPT = kSmpList / kSmpThreads;
+  const int tid = threadIdx.x;
+  u64 w[EPT], ws = 0;
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) {
+    const int e = tid * EPT + i;
+    w[i] = e < n ? mass_of(l[e]) : 0ull;
+    ws += w[i];
+  }
+  if (tid == 0) sh.pos = n;
+  u64 total;
+  u64 run = smp_block_scan(ws, sh.wsum, &total) - ws;
+  const u64 target = target_of(total);
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) {
+    const int e = tid * EPT + i;
+    const u64 next = run + w[i];
+    if (e < n && (by_mass ? (run < target && target <= next) : (u64)(e + 1) == target)) {
+      sh.pos = e;
+      sh.total = next;
+    }
+    run = next;
+  }
+  __syncthreads();
+  const int pos = sh.pos;
+  *through = pos == n ? total : sh.total;
+  __syncthreads();
+  return pos;
+}
+
+// ---------------------------------------------------------------- a contiguous share of a row, in global memory
+// Positions count from a 16-byte boundary at or before the share; those outside it read as -inf.  A warp walks
+// slabs of 128 positions, a contiguous and even number of them.
+template <typename TL>
+struct SmpShare {
+  static constexpr int VE = 16 / sizeof(TL);  // logits of a 16-byte vector
+  const TL* src0;      // position 0
+  int base;            // its row index
+  int p_lo, p_hi;      // the share's positions
+  int slabs, per;      // slabs of the share, and of each warp
+  int warp, lane;
+  BI_DEV SmpShare(const SampleArgs& a, int64_t row, int lo, int n) {
+    const TL* src = static_cast<const TL*>(a.logits) + row * a.ld + lo;
+    p_lo = (int)((reinterpret_cast<uintptr_t>(src) / sizeof(TL)) % VE);
+    p_hi = p_lo + n;
+    base = lo - p_lo;
+    src0 = src - p_lo;
+    slabs = (p_hi + 255) / 256 * 2;
+    per = (slabs / 2 + kSmpWarps - 1) / kSmpWarps * 2;
+    warp = threadIdx.x >> 5;
+    lane = threadIdx.x & 31;
+  }
+  BI_DEV int slab_lo(int w) const { return min(slabs, w * per); }
+  BI_DEV int slab_hi(int w) const { return min(slabs, w * per + per); }
+  BI_DEV static void expand(const uint4& raw, float (&x)[VE]) {
+    const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (VE == 4) {
+        x[i] = __uint_as_float(r[i]);
+      } else {
+        x[2 * i] = bf16lo(r[i]);
+        x[2 * i + 1] = bf16hi(r[i]);
+      }
+    }
+  }
+  template <int N>
+  BI_DEV void edge(int p, float (&x)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = p + i >= p_lo && p + i < p_hi ? (float)src0[p + i] : -INFINITY;
+  }
+  // A lane's four logits of a slab, in index order over the lanes.
+  BI_DEV void slab4(int slab, float (&x)[4]) const { edge<4>(slab * 128 + lane * 4, x); }
+  // visit(first position, four logits) for this warp's slabs (converged), in any order; U vectors in flight
+  template <int U, typename F>
+  BI_DEV void each4(F visit) const {
+    constexpr int STEP = 32 * VE;  // a warp's vector
+    const int p1 = slab_hi(warp) * 128;
+    for (int p = slab_lo(warp) * 128 + lane * VE; p - lane * VE < p1; p += STEP * U) {
+      uint4 raw[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int q = p + j * STEP;
+        if (q >= p_lo && q + VE <= p_hi && q < p1) raw[j] = *reinterpret_cast<const uint4*>(src0 + q);
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int q = p + j * STEP;
+        if (q - lane * VE < p1) {
+          float x[VE];
+          if (q >= p_lo && q + VE <= p_hi) expand(raw[j], x);
+          else edge<VE>(q, x);
+#pragma unroll
+          for (int i = 0; i < VE; i += 4) {
+            const float y[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
+            visit(q + i, y);
+          }
+        }
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------- the rare way: one CTA
+template <typename TL, bool ABS>
+struct SmpSolo {
+  SmpOut out;
+  SmpShare<TL> all;  // the whole row
+  SmpShared& sh;
+  const uint2* tab;
+  u64* list;       // 16 KB: kSmpList entries, or the counters
+  SmpMass<ABS> ms;
+  float x_min;
+  int tid, warp, lane;
+
+  // visit(index, logit)
   template <typename F>
-  BI_DEV void warp_sums(F weight4) {
-    u64 sum = 0;
-    const int s1 = slab_hi(warp);
-    for (int s = slab_lo(warp); s < s1; ++s) {
-      const int p0 = s * 128 + lane * 4;
-      const float4 v = *reinterpret_cast<const float4*>(xs + p0);
-      const float x[4] = {v.x, v.y, v.z, v.w};
-      u64 w[4];
-      weight4(base + p0, x, w);
-      sum += (w[0] + w[1]) + (w[2] + w[3]);
-    }
-    sum = smp_warp_sum(sum);
-    if (lane == 0) sh.wsum[warp] = sum;
+  BI_DEV void each(F visit) {
+    all.template each4<2>([&](int p0, const float (&x)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) visit(all.base + p0 + i, x[i]);
+    });
   }
-  BI_DEV void publish() {
+  // The element, in index order, at which the running weight(index, x) reaches target_of(sum): found(index, x, sum).
+  template <typename F, typename G, typename H>
+  BI_DEV void locate(F weight, G target_of, H found) {
+    u64 w = 0;
+    each([&](int i, float x) { w += weight(i, x); });
+    w = smp_warp_sum(w);
     __syncthreads();
-    if (CS > 1) {
-      if (tid < CS) {
-        u64 t = 0;
-#pragma unroll
-        for (int i = 0; i < kSmpWarps; ++i) t += sh.wsum[i];
-        at(sh.cta_sum, tid)[rank] = t;
-      }
-      csync();
-    } else {
-      if (tid == 0) {
-        u64 t = 0;
-#pragma unroll
-        for (int i = 0; i < kSmpWarps; ++i) t += sh.wsum[i];
-        sh.cta_sum[0] = t;
-      }
-      __syncthreads();
+    if (lane == 0) sh.wsum2[warp] = w;
+    __syncthreads();
+    u64 b = 0, sum = 0;
+    for (int i = 0; i < kSmpWarps; ++i) {
+      if (i < warp) b += sh.wsum2[i];
+      sum += sh.wsum2[i];
     }
+    const u64 target = target_of(sum);
+    if (b < target && target <= b + w) {  // one warp
+      for (int s = all.slab_lo(warp); b < target && s < all.slabs; ++s) {
+        const int i0 = all.base + s * 128 + lane * 4;
+        float x[4];
+        all.slab4(s, x);
+        u64 y[4], inc = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y[i] = weight(i0 + i, x[i]);
+          inc += y[i];
+        }
+        u64 run = inc;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const u64 z = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += z;
+        }
+        run = b + inc - run;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (run < target && target <= run + y[i]) found(i0 + i, x[i], sum);
+          run += y[i];
+        }
+        b += __shfl_sync(0xffffffffu, inc, 31);
+      }
+    }
+    __syncthreads();
   }
-  BI_DEV u64 row_sum() {
-    u64 t = 0;
-#pragma unroll
-    for (int r = 0; r < CS; ++r) t += sh.cta_sum[r];
-    return t;
-  }
-  // After publish(): the element, in index order, at which the running weight reaches target (>= 1); the CTA that
-  // holds it calls found(index, x).  A warp's slabs are taken by a warp each, then the one slab by one warp.
-  template <typename F, typename H>
-  BI_DEV void locate(F weight4, u64 target, H found) {
-    u64 b = 0, mine = 0;
-#pragma unroll
-    for (int r = 0; r < CS; ++r) {
-      const u64 t = sh.cta_sum[r];
-      if (r < rank) b += t;
-      if (r == rank) mine = t;
-    }
-    if (!(b < target && target <= b + mine)) return;
-    int unit = 0;
-    for (; unit < kSmpWarps - 1; ++unit) {
-      const u64 t = sh.wsum[unit];
-      if (target <= b + t) break;
-      b += t;
-    }
-    const int s0 = slab_lo(unit), s1 = slab_hi(unit);
-    for (int sb = s0; sb < s1; sb += kSmpWarps) {  // one round, for up to 16 slabs a warp
-      const int s = sb + warp;
-      float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      const int p0 = s * 128 + lane * 4;
-      u64 y[4] = {0, 0, 0, 0}, inc;
-      if (s < s1) {
-        const float4 v = *reinterpret_cast<const float4*>(xs + p0);
-        x[0] = v.x;
-        x[1] = v.y;
-        x[2] = v.z;
-        x[3] = v.w;
-        weight4(base + p0, x, y);
-      }
-      inc = (y[0] + y[1]) + (y[2] + y[3]);
-      u64 run = inc;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 z = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += z;
-      }
-      run = inc - run;
-      if (lane == 31) sh.wsum2[warp] = inc;
-      __syncthreads();
-      u64 before = b, all = b;
-#pragma unroll
-      for (int i = 0; i < kSmpWarps; ++i) {
-        const u64 t = sh.wsum2[i];
-        if (i < warp) before += t;
-        all += t;
-      }
-      run += before;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (run < target && target <= run + y[i]) found(base + p0 + i, x[i]);
-        run += y[i];
-      }
-      if (target <= all) break;
-      b = all;
-      __syncthreads();
-    }
-  }
-
-  // ---- the cut by histograms with masses, for whatever the quicker ways do not take
-  template <bool ABS>
-  BI_DEV SmpCut select(const SmpMass<ABS>& ms, bool by_mass, bool top_p, u64 target, uint32_t* all_c, u64* all_w) {
-    uint32_t* h = reinterpret_cast<uint32_t*>(list());
+  // The cut at which the running count or mass (top_p: of the mass `target` that is left, 0 for all) reaches target.
+  BI_DEV SmpCut select(bool by_mass, float p, u64 target) {
+    uint32_t* h = reinterpret_cast<uint32_t*>(list);  // counts and four 12-bit limbs of the masses
     uint32_t lo = 0, hi = 0xffffffffu;  // keys of the active elements, once the bins are on keys
-    int bin = -1, shift = 0;            // bin of the octave histogram, then shift of the key histograms
-    int level = 0;
+    int bin = -1, shift = 0, level = 0; // bins of 1/16 octave first
     u64 before_c = 0, before_w = 0;
     while (true) {
       auto active = [&](float x) {
         if (!(x >= x_min)) return false;
         if (level == 0) return true;
-        if (level == 1) return min(ms.bin(x) >> 1, kSmpMassBins - 1) == bin;
+        if (level == 1) return min((ms.k_top - ms.k_of(x)) >> kSmpMassShift, kSmpMassBins - 1) == bin;
         const uint32_t k = smp_key(x);
         return k >= lo && k <= hi;
       };
-      csync();  // the counters' memory is free in every rank
-      for (int i = tid; i < 4 * kSmpMassBins; i += kSmpThreads) h[i] = 0u;
+      __syncthreads();
+      for (int i = tid; i < 5 * kSmpMassBins; i += kSmpThreads) h[i] = 0u;
       __syncthreads();
       each([&](int, float x) {
         if (active(x)) {
-          const int b = level == 0 ? ms.bin(x) >> 1 : (int)((hi - smp_key(x)) >> shift);
+          const int b = level == 0 ? min((ms.k_top - ms.k_of(x)) >> kSmpMassShift, kSmpMassBins - 1) : (int)((hi - smp_key(x)) >> shift);
           const u64 w = ms.mass(x, tab);
           atomicAdd(&h[b], 1u);
-          atomicAdd(&h[kSmpMassBins + b], (uint32_t)w & 0xffffu);
-          atomicAdd(&h[2 * kSmpMassBins + b], (uint32_t)(w >> 16) & 0xffffu);
-          atomicAdd(&h[3 * kSmpMassBins + b], (uint32_t)(w >> 32));
+          // twelve-bit limbs: 2^18 of them sum to less than 2^30
+          atomicAdd(&h[kSmpMassBins + b], (uint32_t)w & 0xfffu);
+          atomicAdd(&h[2 * kSmpMassBins + b], (uint32_t)(w >> 12) & 0xfffu);
+          atomicAdd(&h[3 * kSmpMassBins + b], (uint32_t)(w >> 24) & 0xfffu);
+          atomicAdd(&h[4 * kSmpMassBins + b], (uint32_t)(w >> 36));
         }
       });
-      csync();
-      reduce<kSmpMassBins>(
-          [&](int b, uint32_t& c, u64& w) {
-            for (int r = 0; r < CS; ++r) {
-              const uint32_t* g = at(h, r);
-              c += g[b];
-              w += (u64)g[kSmpMassBins + b] + ((u64)g[2 * kSmpMassBins + b] << 16) +
-                   ((u64)g[3 * kSmpMassBins + b] << 32);
-            }
-          },
-          [&](int b, uint32_t c, u64 w) {
-            h[b] = c;
-            h[kSmpMassBins + b] = (uint32_t)w;
-            h[2 * kSmpMassBins + b] = (uint32_t)(w >> 32);
-          });
-      if (level == 0) {
-        *all_c = tot_c;
-        *all_w = tot_w;
-        if (top_p) target = top_p_target(target ? target : tot_w);  // target: the mass that top-k left, or 0
-      }
-      const SmpFind f = find<kSmpMassBins>(by_mass, target - (by_mass ? before_w : before_c),
-                                           [&](int b, uint32_t& c, u64& w) {
-                                             c = h[b];
-                                             w = (u64)h[2 * kSmpMassBins + b] << 32 | h[kSmpMassBins + b];
-                                           });
-      if (f.bin < 0) return SmpCut{smp_key(x_min), 0x7fffffff, tot_w};  // fewer elements than asked for: all stay
+      __syncthreads();
+      static_assert(kSmpMassBins == kSmpThreads, "a bin per thread");
+      const uint32_t c = h[tid];
+      const u64 w = (u64)h[kSmpMassBins + tid] + ((u64)h[2 * kSmpMassBins + tid] << 12) +
+                    ((u64)h[3 * kSmpMassBins + tid] << 24) + ((u64)h[4 * kSmpMassBins + tid] << 36);
+      u64 tot_c, tot_w;
+      const u64 ic = smp_block_scan(c, sh.wsum, &tot_c);
+      const u64 iw = smp_block_scan(w, sh.wsum, &tot_w);
+      if (level == 0 && by_mass) target = smp_top_p_target(p, target ? target : tot_w);
+      const u64 want = target - (by_mass ? before_w : before_c);
+      if (want > (by_mass ? tot_w : tot_c)) return SmpCut{smp_key(x_min), 0x7fffffff, tot_w};  // too few: all stay
+      if (by_mass ? (iw - w < want && want <= iw) : (ic - c < want && want <= ic))
+        sh.find = SmpFind{tid, (uint32_t)(ic - c), c, iw - w, w};
+      __syncthreads();
+      const SmpFind f = sh.find;
       before_c += f.before;
       before_w += f.before_mass;
       if (level == 0) {
         bin = f.bin;
       } else {
         hi = hi - ((uint32_t)f.bin << shift);
-        const uint32_t width = (1u << shift) - 1u;
-        lo = hi - min(width, hi - lo);
+        lo = hi - min((1u << shift) - 1u, hi - lo);
       }
       ++level;
-      if (level == 1 || f.inside > (uint32_t)kSmpList) {
-        // smallest and largest key of the bin
+      if (level == 1 || f.inside > (uint32_t)kSmpList) {  // smallest and largest key of the bin
         uint32_t kmin = 0xffffffffu, kmax = 0u;
         each([&](int, float x) {
           if (active(x)) {
@@ -756,422 +658,217 @@ struct SmpRow {
         });
         kmin = __reduce_min_sync(0xffffffffu, kmin);
         kmax = __reduce_max_sync(0xffffffffu, kmax);
+        __syncthreads();
         if (lane == 0) {
           sh.wcnt[warp] = kmin;
           sh.wsum[warp] = kmax;
         }
         __syncthreads();
-        par ^= 1;
-        if (tid == 0) {
-          for (int i = 0; i < kSmpWarps; ++i) {
-            kmin = min(kmin, sh.wcnt[i]);
-            kmax = max(kmax, (uint32_t)sh.wsum[i]);
-          }
-          sh.pub_lo[par] = kmin;
-          sh.pub_hi[par] = kmax;
-        }
-        csync();
-        for (int r = 0; r < CS; ++r) {
-          kmin = min(kmin, *at(&sh.pub_lo[par], r));
-          kmax = max(kmax, *at(&sh.pub_hi[par], r));
+        for (int i = 0; i < kSmpWarps; ++i) {
+          kmin = min(kmin, sh.wcnt[i]);
+          kmax = max(kmax, (uint32_t)sh.wsum[i]);
         }
         lo = kmin;
         hi = kmax;
         level = 2;
-        shift = max(0, 32 - __clz(kmax - kmin) - 10);
+        shift = max(0, 32 - __clz(kmax - kmin) - kSmpMassBits);
       }
       const u64 left = target - (by_mass ? before_w : before_c);
       if (lo == hi) {  // equal values: the first `need` of them by index
         const float x1 = smp_unkey(lo);
         const u64 w1 = ms.mass(x1, tab);
         const u64 need = by_mass ? (left + w1 - 1) / w1 : left;  // a bin that mass reached has some
-        auto one = [&](int, const float (&x)[4], u64 (&w)[4]) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = x[i] >= x_min && x[i] == x1 ? 1ull : 0ull;
-        };
-        warp_sums(one);
-        publish();
-        locate(one, need, [&](int i, float) {
-          for (int r = 0; r < CS; ++r) at(&sh.cut, r)->idx = i;
-        });
-        csync();
-        const SmpCut c{lo, sh.cut.idx, before_w + need * w1};
-        csync();
-        return c;
+        locate([&](int, float x) { return x >= x_min && x == x1 ? 1ull : 0ull; }, [&](u64) { return need; },
+               [&](int i, float, u64) { sh.pos = i; });
+        return SmpCut{lo, sh.pos, before_w + need * w1};
       }
       if (f.inside <= (uint32_t)kSmpList) {
-        u64* l = at(list(), 0);
-        uint32_t* n = at(&sh.list_n, 0);
+        __syncthreads();
         if (tid == 0) sh.list_n = 0;
-        csync();
-        each([&](int pos, float x) {
-          if (active(x)) l[atomicAdd(n, 1u)] = entry(x, pos);
+        __syncthreads();
+        each([&](int i, float x) {
+          if (active(x)) list[atomicAdd(&sh.list_n, 1u)] = smp_entry(x, i);
         });
-        csync();
-        if (rank == 0) {
-          sort((int)f.inside);
-          u64 through;
-          const int pos = list_find((int)f.inside, by_mass, [&](u64 e) { return ms.mass(entry_x(e), tab); },
-                                    [&](u64) { return left; }, &through);
-          if (tid == 0) {
-            const u64 e = list()[pos];
-            const SmpCut c{~(uint32_t)(e >> 32), (int32_t)(uint32_t)e, before_w + through};
-            for (int r = 0; r < CS; ++r) *at(&sh.cut, r) = c;
-          }
-        }
-        csync();
-        const SmpCut c = sh.cut;
-        csync();
-        return c;
+        __syncthreads();
+        smp_sort(list, (int)f.inside);
+        u64 through;
+        const int pos = smp_list_find(sh, list, (int)f.inside, by_mass,
+                                      [&](u64 e) { return ms.mass(smp_entry_x(e), tab); }, [&](u64) { return left; },
+                                      &through);
+        const u64 e = list[pos];
+        return SmpCut{~(uint32_t)(e >> 32), (int32_t)(uint32_t)e, before_w + through};
       }
     }
   }
-  template <bool ABS>
-  __device__ __noinline__ SmpCut general(SmpMass<ABS> ms) {
-    uint32_t all_c;
-    u64 all_w;
+  BI_DEV void run() {
+    tid = threadIdx.x;
+    warp = tid >> 5;
+    lane = tid & 31;
     SmpCut cut{smp_key(x_min), 0x7fffffff, 0ull};
     u64 left = 0;
-    if (k_eff < a.V) {
-      cut = select(ms, false, false, (u64)k_eff, &all_c, &all_w);
+    if (sh.k_eff < out.a.V) {
+      cut = select(false, 1.f, (u64)sh.k_eff);
       left = cut.mass;
+      __syncthreads();
     }
-    if (p < 1.f) {
-      const SmpCut c = select(ms, true, true, left, &all_c, &all_w);
+    if (sh.p < 1.f) {
+      const SmpCut c = select(true, sh.p, left);
       if (c.key > cut.key || (c.key == cut.key && c.idx < cut.idx)) cut = c;
+      __syncthreads();
     }
-    return cut;
+    const float cut_x = smp_unkey(cut.key);
+    const int32_t id = sh.id;
+    locate([&](int i, float x) { return x > cut_x || (x == cut_x && i <= cut.idx) ? ms.mass(x, tab) : 0ull; },
+           [&](u64 S) { return out.a.ids_in ? S : smp_draw_target(sh.u, S); },
+           [&](int i, float x, u64 S) {
+             if (!out.a.ids_in) out.token(ms, sh, tab, i, x, S);
+             else sh.total2 = S;
+           });
+    if (out.a.ids_in && tid == 0) {
+      const float x = sh.x_id;
+      if (x > cut_x || (x == cut_x && id <= cut.idx)) out.token(ms, sh, tab, id, x, sh.total2);
+      else out.write(id, -INFINITY);
+    }
+  }
+};
+template <typename TL, bool ABS>
+__device__ __noinline__ void smp_solo(SmpOut out, SmpShared& sh, const uint2* tab, u64* list, SmpMass<ABS> ms,
+                                      float x_min) {
+  SmpSolo<TL, ABS> r{out, SmpShare<TL>(out.a, out.row, 0, out.a.V), sh, tab, list, ms, x_min};
+  r.run();
+}
+
+// ---------------------------------------------------------------- one row per cluster of CS CTAs
+template <typename TL, int CS>
+struct SmpRow {
+  SmpOut out;
+  SmpShare<TL> mine;   // this CTA's part of the row
+  SmpShared& sh;
+  uint2* table;        // [64][kSmpTabLanes]
+  const uint2* tab;    // this lane's copy of it
+  unsigned char* area; // 8 KB: counts; 16 KB: list
+  cg::cluster_group cl;
+  int tid, warp, lane, rank;
+  float m, x_min;      // row maximum; smallest logit that min-p keeps (above -inf)
+  bool score;
+
+  BI_DEV uint32_t* counts() { return reinterpret_cast<uint32_t*>(area); }
+  BI_DEV u64* list() { return reinterpret_cast<u64*>(area + 8192); }
+  static constexpr int kSegment = kSmpList / CS;  // a CTA's part of rank 0's list
+
+  BI_DEV void csync() {
+    if (CS == 1) __syncthreads();
+    else cl.sync();
+  }
+  template <typename P>
+  BI_DEV P* at(P* ptr, int r) {
+    if (CS == 1) return ptr;
+    return cl.map_shared_rank(ptr, r);
+  }
+  // Appends (warp-converged) to this CTA's segment of rank 0's list; entries beyond it are counted only.
+  BI_DEV void append(bool take, float x, int pos, u64* segment, u64* own) {
+    const unsigned who = __ballot_sync(0xffffffffu, take);
+    if (who == 0u) return;
+    uint32_t o = 0;
+    if (lane == 0) o = atomicAdd(&sh.list_n, (uint32_t)__popc(who));
+    o = __shfl_sync(0xffffffffu, o, 0) + __popc(who & ((1u << lane) - 1u));
+    if (take && o < (uint32_t)kSegment) {
+      const u64 e = smp_entry(x, mine.base + pos);
+      segment[o] = e;
+      if (own) own[o] = e;
+    }
+  }
+  // Rank 0: the segments' entries joined at the front of the list (no barrier after it); their number, or -1 when
+  // a segment overflowed.
+  BI_DEV int join() {
+    u64* l = list();
+    uint32_t n = 0;
+    bool fits = true;
+#pragma unroll
+    for (int r = 0; r < CS; ++r) {
+      const uint32_t nr = sh.cta_n[r];
+      fits = fits && nr <= (uint32_t)kSegment;
+      if (r > 0 && fits)  // moves down: a segment never starts before the entries so far end
+        for (uint32_t i0 = 0; i0 < nr; i0 += kSmpThreads) {
+          const bool mine_too = i0 + tid < nr;
+          const u64 e = mine_too ? l[r * kSegment + i0 + tid] : 0ull;
+          __syncthreads();
+          if (mine_too) l[n + i0 + tid] = e;
+        }
+      n += nr;
+    }
+    __syncthreads();
+    return fits ? (int)n : -1;
   }
 
-  // ---- top-k up to kSmpMaxK: candidates by the threads' maxima.  False: too many of them.
-  template <bool ABS>
-  BI_DEV bool few(const SmpMass<ABS>& ms, float t_max, float row_min) {
-    // bins linear in x, from the row's maximum to the smallest of the threads' maxima (counts() is zeroed)
-    const float scale = fminf(__fdiv_rn((float)(kSmpMaxBins - 2), __fsub_rn(m, row_min)), FLT_MAX);
-    if (t_max >= x_min) {
-      const float y = __fmul_rn(__fsub_rn(m, t_max), scale);
-      atomicAdd(&counts()[y < (float)(kSmpMaxBins - 1) ? (int)y : kSmpMaxBins - 1], 1u);
-    }
-    csync();
-    if (warp == 0) {
-      // lane l sums bins 8 l .. 8 l + 7 of the cluster's CTAs
-      uint32_t c[8], n = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = 0;
-#pragma unroll
-      for (int r = 0; r < CS; ++r) {
-        const uint4* q = reinterpret_cast<const uint4*>(at(counts(), r)) + lane * 2;
-        const uint4 v0 = q[0], v1 = q[1];
-        c[0] += v0.x;
-        c[1] += v0.y;
-        c[2] += v0.z;
-        c[3] += v0.w;
-        c[4] += v1.x;
-        c[5] += v1.y;
-        c[6] += v1.z;
-        c[7] += v1.w;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) n += c[i];
-      uint32_t inc = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      uint32_t run = inc - n;
-      int bin = kSmpMaxBins - 1;  // fewer maxima than k: every logit is a candidate
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (run < (uint32_t)k_eff && (uint32_t)k_eff <= run + c[i]) bin = lane * 8 + i;
-        run += c[i];
-      }
-      bin = __reduce_min_sync(0xffffffffu, bin);
-      // k_eff of the maxima lie in the bins up to this one, so the k_eff largest logits are not below its end
-      // (made lower by more than the roundings above)
-      if (lane == 0) {
-        const float depth = __fmul_rn(__fdiv_rn((float)(bin + 1), scale), 1.000001f);
-        sh.x_cut = bin == kSmpMaxBins - 1 ? x_min : fmaxf(x_min, __fsub_rd(m, depth));
-      }
-    }
-    __syncthreads();
-    const float x_cut = sh.x_cut;
-    uint32_t* n = at(&sh.list_n, 0);
-    u64* l = at(list(), 0);
-    const int s1 = slab_hi(warp);
-    for (int s = slab_lo(warp); s < s1; ++s) {
-      const int p0 = s * 128 + lane * 4;
-      const float4 v = *reinterpret_cast<const float4*>(xs + p0);
-      const float top = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-      if (__any_sync(0xffffffffu, top >= x_cut)) {
-        append(v.x >= x_cut, v.x, p0, n, l, kSmpList);
-        append(v.y >= x_cut, v.y, p0 + 1, n, l, kSmpList);
-        append(v.z >= x_cut, v.z, p0 + 2, n, l, kSmpList);
-        append(v.w >= x_cut, v.w, p0 + 3, n, l, kSmpList);
-      }
-    }
-    csync();
-    const uint32_t total = *n;
-    if (total > (uint32_t)kSmpList) return false;
-    if (rank == 0) {
-      if (total <= (uint32_t)kSmpThreads / 4) small<4>(ms, (int)total);
-      else if (total <= (uint32_t)kSmpThreads) small<1>(ms, (int)total);
-      else {
-        SmpRow other = *this;  // as in finish()
-        other.small_sorted(ms, (int)total);
-      }
-    }
-    return true;
-  }
-  // The row's kept set lies in the list of at most kSmpThreads entries (one CTA): G threads (or one) per entry sum
-  // what comes before it in order, then in index order.
-  template <int G, typename F>
-  BI_DEV u64 sum_before(int n, int g, const u64* wl, F before, int* count) {
-    const u64* l = list();
-    u64 w = 0;
-    int c = 0;
-#pragma unroll 4
-    for (int j = g; j < n; j += G) {
-      const u64 y = wl[j];
-      if (before(l[j])) {
-        w += y;
-        ++c;
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < G; o <<= 1) {
-      w += __shfl_xor_sync(0xffffffffu, w, o);
-      c += __shfl_xor_sync(0xffffffffu, c, o);
-    }
-    *count = c;
-    return w;
-  }
-  template <int G, bool ABS>
-  BI_DEV void small(const SmpMass<ABS>& ms, int n) {
-    u64* l = list();
-    u64* wl = l + kSmpThreads;
-    const int i = tid / G, g = tid % G;
-    const bool mine = i < n;
-    const u64 e = mine ? l[i] : 0ull;
-    const float x = entry_x(e);
-    u64 w = mine ? ms.mass(x, tab) : 0ull;
-    if (g == 0) wl[i] = w;
-    if (tid == 0) sh.total2 = 0ull;
-    __syncthreads();
-    const int k = min(n, k_eff);
-    int before = 0;
-    u64 before_w = 0;
-    if (warp * 32 / G < n) {
-      before_w = sum_before<G>(n, g, wl, [&](u64 y) { return y < e; }, &before);
-      if (mine && before == k - 1) sh.total = before_w + w;  // the mass that top-k leaves
-    }
-    __syncthreads();
-    bool kept = mine && before < k;
-    if (p < 1.f) {
-      const u64 target = top_p_target(sh.total);
-      kept = kept && before_w < target;
-      if (kept && target <= before_w + w) sh.total2 = before_w + w;
-    }
-    if (!kept) w = 0;
-    if (g == 0) wl[i] = w;
-    const bool it = kept && score && (int32_t)(uint32_t)e == sh.id && g == 0;
-    const int any = __syncthreads_or(it);
-    const u64 S = p < 1.f ? sh.total2 : sh.total;
-    if (score) {
-      if (it) write_token(ms, sh.id, x, S);
-      if (!any && tid == 0) write(sh.id, -INFINITY);  // cut off, or not among the candidates
-    } else if (warp * 32 / G < n) {
-      const u64 run = sum_before<G>(n, g, wl, [&](u64 y) { return (uint32_t)y < (uint32_t)e; }, &before);
-      const u64 target = draw_target(S);
-      if (g == 0 && run < target && target <= run + w) write_token(ms, (int32_t)(uint32_t)e, x, S);
-    }
-  }
-  // The same for up to kSmpList entries, by sorts.
-  template <bool ABS>
-  __device__ __noinline__ void small_sorted(SmpMass<ABS> ms, int n) {
-    u64* l = list();
-    sort(n);
-    n = min(n, k_eff);
-    u64 S;
-    int last = list_find(n, true, [&](u64 e) { return ms.mass(entry_x(e), tab); },
-                         [&](u64 total) { return p < 1.f ? top_p_target(total) : total + 1ull; }, &S);
-    if (last == n) last = n - 1;  // no top-p: all of them, with or without mass
-    if (score) {
-      const u64 e = (u64)(~smp_key(sh.x_id)) << 32 | (uint32_t)sh.id;
-      if (tid == 0) {
-        if (e <= l[last]) write_token(ms, sh.id, sh.x_id, S);
-        else write(sh.id, -INFINITY);
-      }
-      return;
-    }
-    // index order: (index, mass) in one key (18 and 46 bits)
-    for (int i = tid; i <= last; i += kSmpThreads) {
-      const u64 e = l[i];
-      l[i] = (e << 46) | ms.mass(entry_x(e), tab);
-    }
-    __syncthreads();
-    sort(last + 1);
-    u64 through;
-    const int pos = list_find(last + 1, true, [&](u64 e) { return e & ((1ull << 46) - 1ull); },
-                              [&](u64 total) { return draw_target(total); }, &through);
-    if (tid == 0) {
-      const int32_t best = (int32_t)(l[pos] >> 46);
-      write_token(ms, best, value(best), S);
-    }
-  }
-
-  // ---- top-p over the whole row: predicted cut, exact sums.  False: the prediction missed, or a list is full.
-  template <bool ABS>
-  BI_DEV bool nucleus(const SmpMass<ABS>& ms) {
-    for (int i = tid; i < kSmpBins; i += kSmpThreads) counts()[i] = 0u;
-    __syncthreads();
-    each([&](int, float x) {
-      const int b = ms.k_top - ms.k_of(x);
-      if (x >= x_min && b < kSmpBins - 1) atomicAdd(&counts()[b], 1u);  // the open bin would only serialise
-    });
-    csync();
-    // a bin's mass is about its count times 2^(k / 64); the open bin's is left out of the prediction
-    u64* est = list();
-    reduce<kSmpBins>(
-        [&](int b, uint32_t& c, u64& w) {
-#pragma unroll
-          for (int r = 0; r < CS; ++r) c += at(counts(), r)[b];
-          const int k = ms.k_top - b;
-          if (b < kSmpBins - 1) w = ((u64)c * kExp2Tab[k & 63]) << kSmpFrac >> (ms.oct_top - (k >> 6));
-        },
-        [&](int b, uint32_t, u64 w) { est[b - rank * (kSmpBins / CS)] = w; });
-    __syncthreads();
-    const u64 guess = top_p_target(tot_w);
-    const SmpFind f = find<kSmpBins>(true, guess, [&](int b, uint32_t& c, u64& w) {
-      c = 0;
-      w = est[b - rank * (kSmpBins / CS)];
-    });
-    if (f.bin < 0 || f.bin >= kSmpBins - 2) return false;
-    // a bin of many logits is cut at the fraction of its mass that is still wanted, to within 0.15 of it;
-    // one of few, anywhere in it or next to it
-    const float k_bin = (float)(ms.k_top - f.bin);
-    float hi = k_bin + 1.5f, lo = k_bin - 1.5f;
-    if (f.inside_mass >= 64ull * ((u64)kExp2Tab[(ms.k_top - f.bin) & 63] << kSmpFrac >>
-                                  (ms.oct_top - ((ms.k_top - f.bin) >> 6)))) {
-      const float mid = k_bin + 0.5f - __fdiv_rn((float)(guess - f.before_mass), (float)f.inside_mass);
-      hi = mid + 0.15f;
-      lo = mid - 0.15f;
-    }
-    const float x_lo = fmaxf(x_min, ABS ? __fdiv_rn(lo, ms.c_hi) : __fadd_rn(m, __fdiv_rn(lo, ms.c_hi)));
-    const float x_hi = fmaxf(x_lo, ABS ? __fdiv_rn(hi, ms.c_hi) : __fadd_rn(m, __fdiv_rn(hi, ms.c_hi)));
-    u64 all = 0, above = 0;
-    const int s1 = slab_hi(warp);
-    u64* ml = CS == 1 ? list() : own_list();
-    constexpr uint32_t cap = CS == 1 ? kSmpList : kSmpLocal;
-    for (int s = slab_lo(warp); s < s1; ++s) {
-      const int p0 = s * 128 + lane * 4;
-      const float4 v = *reinterpret_cast<const float4*>(xs + p0);
-      const float x[4] = {v.x, v.y, v.z, v.w};
-      bool near = false;
+  // ---- sums over the row, and the draw.  weight4(index of the first, x, w) gives four elements' weights.
+  // Warp sums to sh.wsum; then, with publish(), the CTA's sum to every rank's sh.cta_sum.
+  template <typename F>
+  BI_DEV void warp_sums(F weight4) {
+    u64 sum = 0;
+    mine.template each4<4>([&](int p0, const float (&x)[4]) {
       u64 w[4];
-      ms.mass4(x, tab, w);
+      weight4(mine.base + p0, x, w);
+      sum += (w[0] + w[1]) + (w[2] + w[3]);
+    });
+    sum = smp_warp_sum(sum);
+    if (lane == 0) sh.wsum[warp] = sum;
+  }
+  BI_DEV void publish() {
+    __syncthreads();
+    if (tid < CS) {
+      u64 t = 0;
+#pragma unroll
+      for (int i = 0; i < kSmpWarps; ++i) t += sh.wsum[i];
+      at(sh.cta_sum, tid)[rank] = t;
+    }
+    csync();
+  }
+  BI_DEV u64 row_sum() {
+    u64 t = 0;
+#pragma unroll
+    for (int r = 0; r < CS; ++r) t += sh.cta_sum[r];
+    return t;
+  }
+  // After publish(): the element, in index order, at which the running weight reaches target (>= 1); the CTA that
+  // holds it calls found(index, x).  Its warp's slabs are taken by a warp each.
+  template <typename F, typename H>
+  BI_DEV void locate(F weight4, u64 target, H found) {
+    u64 b = 0, own = 0;
+#pragma unroll
+    for (int r = 0; r < CS; ++r) {
+      const u64 t = sh.cta_sum[r];
+      if (r < rank) b += t;
+      if (r == rank) own = t;
+    }
+    if (!(b < target && target <= b + own)) return;
+    int unit = 0;
+    for (; unit < kSmpWarps - 1; ++unit) {
+      const u64 t = sh.wsum[unit];
+      if (target <= b + t) break;
+      b += t;
+    }
+    const int s1 = mine.slab_hi(unit);
+    for (int sb = mine.slab_lo(unit); sb < s1; sb += kSmpWarps) {
+      const int i0 = mine.base + (sb + warp) * 128 + lane * 4;
+      float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      u64 y[4] = {0, 0, 0, 0};
+      if (sb + warp < s1) {
+        mine.slab4(sb + warp, x);
+        weight4(i0, x, y);
+      }
+      const u64 y4 = (y[0] + y[1]) + (y[2] + y[3]);
+      u64 all;
+      u64 run = b + smp_block_scan(y4, sh.wsum2, &all) - y4;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (x[i] >= x_min) all += w[i];
-        if (x[i] > x_hi) above += w[i];
-        near |= x[i] <= x_hi && x[i] >= x_lo;
+        if (run < target && target <= run + y[i]) found(i0 + i, x[i]);
+        run += y[i];
       }
-      if (__any_sync(0xffffffffu, near)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) append(x[i] <= x_hi && x[i] >= x_lo, x[i], p0 + i, &sh.list_n, ml, cap);
-      }
-    }
-    all = smp_warp_sum(all);
-    above = smp_warp_sum(above);
-    if (lane == 0) {
-      sh.wsum[warp] = all;
-      sh.wsum2[warp] = above;
-    }
-    csync();
-    // rank 0 collects the sums and the lists
-    if (rank == 0) {
-      if (warp == 0) {
-        u64 t = 0, t2 = 0;
-        for (int g = lane; g < CS * kSmpWarps; g += 32) {
-          t += at(sh.wsum, g / kSmpWarps)[g % kSmpWarps];
-          t2 += at(sh.wsum2, g / kSmpWarps)[g % kSmpWarps];
-        }
-        t = smp_warp_sum(t);
-        t2 = smp_warp_sum(t2);
-        if (lane == 0) {
-          sh.total = t;
-          sh.total2 = t2;
-        }
-      }
-      uint32_t n = 0;
-      bool fits = true;
-#pragma unroll
-      for (int r = 0; r < CS; ++r) {
-        const uint32_t nr = *at(&sh.list_n, r);
-        fits = fits && nr <= cap && n + nr <= (uint32_t)kSmpList;
-        if (CS > 1 && fits)
-          for (uint32_t i = tid; i < nr; i += kSmpThreads) list()[n + i] = at(own_list(), r)[i];
-        n += nr;
-      }
-      __syncthreads();
-      const u64 over = sh.total2, target = top_p_target(sh.total);
-      if (tid == 0) sh.cut = SmpCut{0u, -1, 0ull};
-      __syncthreads();
-      if (fits && over < target) list_cut(ms, (int)n, over, target);
-      __syncthreads();
-      const SmpCut c = sh.cut;
-      if (tid < CS && tid > 0) *at(&sh.cut, tid) = c;
-      if (score && c.idx >= 0 && tid == 0) {
-        const u64 e = (u64)(~smp_key(sh.x_id)) << 32 | (uint32_t)sh.id;
-        if (e <= ((u64)(~c.key) << 32 | (uint32_t)c.idx)) write_token(ms, sh.id, sh.x_id, c.mass);
-        else write(sh.id, -INFINITY);
-      }
-    }
-    csync();
-    const SmpCut cut = sh.cut;
-    if (cut.idx < 0) return false;
-    if (score) return true;
-    // the warps' kept sums: what lies above the list, and the list's kept entries
-    const u64 last = (u64)(~cut.key) << 32 | (uint32_t)cut.idx;
-    for (uint32_t i = tid; i < sh.list_n; i += kSmpThreads) {
-      const u64 e = ml[i];
-      if (e <= last) atomicAdd(&sh.wsum2[((int)(uint32_t)e - base) / 128 / per], ms.mass(entry_x(e), tab));
-    }
-    __syncthreads();
-    if (tid < kSmpWarps) sh.wsum[tid] = sh.wsum2[tid];
-    publish();
-    draw(ms, cut);
-    return true;
-  }
-  // The entry of list[0, n) at which the mass in order, from `over` on, reaches target, to sh.cut (one CTA).
-  template <bool ABS>
-  BI_DEV void list_cut(const SmpMass<ABS>& ms, int n, u64 over, u64 target) {
-    u64* l = list();
-    if (n <= kSmpThreads) {
-      u64* wl = l + kSmpThreads;
-      const u64 e = tid < n ? l[tid] : 0ull;
-      const u64 w = tid < n ? ms.mass(entry_x(e), tab) : 0ull;
-      wl[tid] = w;
-      __syncthreads();
-      if (warp * 32 < n) {
-        u64 run = over;
-        for (int j = 0; j < n; ++j)
-          if (l[j] < e) run += wl[j];
-        if (tid < n && run < target && target <= run + w)
-          sh.cut = SmpCut{~(uint32_t)(e >> 32), (int32_t)(uint32_t)e, run + w};
-      }
-    } else {
-      sort(n);
-      u64 through;
-      const int pos = list_find(n, true, [&](u64 e) { return ms.mass(entry_x(e), tab); },
-                                [&](u64) { return target - over; }, &through);
-      if (tid == 0 && pos < n) {
-        const u64 e = l[pos];
-        sh.cut = SmpCut{~(uint32_t)(e >> 32), (int32_t)(uint32_t)e, over + through};
-      }
+      b += all;
+      if (target <= b) break;
     }
   }
-
   template <bool ABS>
   struct Kept {  // masses of the kept elements
     const SmpMass<ABS>& ms;
@@ -1187,50 +884,438 @@ struct SmpRow {
   };
   // The draw from the kept set, after publish().
   template <bool ABS>
-  BI_DEV void draw(const SmpMass<ABS>& ms, const SmpCut& cut) {
+  BI_DEV void draw(const SmpMass<ABS>& ms, float cut_x, int32_t cut_i) {
     const u64 S = row_sum();
-    locate(Kept<ABS>{ms, tab, smp_unkey(cut.key), cut.idx}, draw_target(S),
-           [&](int i, float x) { write_token(ms, i, x, S); });
+    locate(Kept<ABS>{ms, tab, cut_x, cut_i}, smp_draw_target(sh.u, S),
+           [&](int i, float x) { out.token(ms, sh, tab, i, x, S); });
   }
 
-  // False: nothing in this CTA's shared memory is reached by others any more.
-  template <bool ABS>
-  BI_DEV bool finish(float t_max, float row_min) {
-    SmpMass<ABS> ms;
-    ms.init(m, sh.c_hi, sh.c_lo);
-    SmpCut cut{smp_key(x_min), 0x7fffffff, 0ull};
-    if (k_eff < a.V || p < 1.f) {
-      if constexpr (ABS) {
-        if (k_eff < a.V && k_eff <= kSmpMaxK) {
-          if (few(ms, t_max, row_min)) return true;
-        } else if (k_eff == a.V) {
-          if (nucleus(ms)) return true;
-        }
+  // ---- what follows from the row's maximum; false: the row is answered (rank 0)
+  BI_DEV bool row_max() {
+    float mx = sh.cta_max[0];
+#pragma unroll
+    for (int r = 1; r < CS; ++r) mx = smp_max_nan(mx, sh.cta_max[r]);
+    m = mx;
+    const bool bad = !(m < INFINITY);  // NaN or +inf
+    if (bad || m == -INFINITY) {
+      if (rank == 0 && tid == 0) {
+        if (bad) report(out.a.status, DEV_BAD_VALUE);
+        out.write(-1, bad ? NAN : -INFINITY);
       }
-      SmpRow other = *this;  // the rare way's own copy, so that this one stays in registers
-      cut = other.general(ms);
-      if (score) {
-        if (rank == 0 && tid == 0) {
-          const u64 e = (u64)(~smp_key(sh.x_id)) << 32 | (uint32_t)sh.id;
-          if (e <= ((u64)(~cut.key) << 32 | (uint32_t)cut.idx)) write_token(ms, sh.id, sh.x_id, cut.mass);
-          else write(sh.id, -INFINITY);
-        }
-        return true;
-      }
-      warp_sums(Kept<ABS>{ms, tab, smp_unkey(cut.key), cut.idx});
-    } else if (x_min == -FLT_MAX) {
-      warp_sums([&](int, const float (&x)[4], u64 (&w)[4]) { ms.mass4(x, tab, w); });
-    } else {
-      warp_sums(Kept<ABS>{ms, tab, x_min, 0x7fffffff});
+      return false;
     }
-    publish();
-    if (!score) draw(ms, cut);
-    else if (rank == 0 && tid == 0) write_token(ms, sh.id, sh.x_id, row_sum());
-    return false;
+    // the smallest float whose mass is at least min_p
+    const float mp = sh.min_p;
+    x_min = -FLT_MAX;
+    if (mp >= 1.f) x_min = m;
+    else if (mp > 0.f) x_min = fmaxf(-FLT_MAX, __double2float_ru((double)m + sh.log_min_p));
+    if (score && !(sh.x_id >= x_min)) {
+      if (rank == 0 && tid == 0) out.write(sh.id, -INFINITY);
+      return false;
+    }
+    return true;
+  }
+  BI_DEV bool absolute() { return fabsf(m) * sh.c_hi < 524288.f; }
+  BI_DEV void solo() {
+    if (absolute()) {
+      SmpMass<true> ms;
+      ms.init(m, sh);
+      smp_solo<TL>(out, sh, tab, list(), ms, x_min);
+    } else {
+      SmpMass<false> ms;
+      ms.init(m, sh);
+      smp_solo<TL>(out, sh, tab, list(), ms, x_min);
+    }
   }
 
-  // The row's parameters and constants, by one thread.
-  BI_DEV void setup() {
+  // ---- top-k up to kSmpMaxK.  k: the CTA's bound is the k-th largest of its threads' maxima.
+  BI_DEV void few(int k, float t_max, float cta_max, float cta_min) {
+    // bins linear in x, from the CTA's maximum to the smallest of the threads' maxima (counts() is zeroed)
+    const float scale = fminf(__fdiv_rn((float)(kSmpMaxBins - 2), __fsub_rn(cta_max, cta_min)), FLT_MAX);
+    if (t_max > -INFINITY) {
+      const float y = __fmul_rn(__fsub_rn(cta_max, t_max), scale);
+      atomicAdd(&counts()[y < (float)(kSmpMaxBins - 1) ? (int)y : kSmpMaxBins - 1], 1u);
+    }
+    __syncthreads();
+    // lane l holds bins 8 l .. 8 l + 7 (every warp for itself)
+    uint32_t c[8], n = 0;
+    *reinterpret_cast<uint4*>(c) = reinterpret_cast<const uint4*>(counts())[lane * 2];
+    *reinterpret_cast<uint4*>(c + 4) = reinterpret_cast<const uint4*>(counts())[lane * 2 + 1];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n += c[i];
+    uint32_t run = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += y;
+    }
+    run -= n;
+    int bin = kSmpMaxBins - 1;  // fewer maxima than k: every logit is let through
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (run < (uint32_t)k && (uint32_t)k <= run + c[i]) bin = lane * 8 + i;
+      run += c[i];
+    }
+    bin = __reduce_min_sync(0xffffffffu, bin);
+    // k of the maxima lie in the bins up to this one: none is below its end (made lower by more than the roundings)
+    const float depth = __fmul_rn(__fdiv_rn((float)(bin + 1), scale), 1.000001f);
+    const float bound = bin == kSmpMaxBins - 1 ? -FLT_MAX : fmaxf(-FLT_MAX, __fsub_rd(cta_max, depth));
+    u64* segment = at(list(), 0) + rank * kSegment;
+    mine.template each4<4>([&](int p0, const float (&x)[4]) {
+      const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      if (__any_sync(0xffffffffu, top >= bound)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) append(x[i] >= bound, x[i], p0 + i, segment, nullptr);
+      }
+    });
+    __syncthreads();
+    if (tid == 0) {
+      at(sh.cta_n, 0)[rank] = sh.list_n;
+      at(sh.cta_max, 0)[rank] = cta_max;
+      at(sh.cta_bound, 0)[rank] = bound;
+    }
+    csync();
+    if (rank > 0) return;
+    if (!row_max()) return;
+    const int total = join();
+    bool done = false;
+    if (total >= 0 && absolute()) {
+      float need = sh.cta_bound[0];  // every logit that is not below this is in the list
+#pragma unroll
+      for (int r = 1; r < CS; ++r) need = fmaxf(need, sh.cta_bound[r]);
+      SmpMass<true> ms;
+      ms.init(m, sh);
+      done = total <= kSmpThreads ? small(ms, total, need) : small_sorted(ms, total, need);
+    }
+    if (!done) solo();
+  }
+  // The row's kept set lies in the list of n entries, a thread each (rank 0).  False: it may not.
+  BI_DEV bool small(const SmpMass<true>& ms, int n, float need) {
+    u64* l = list();
+    u64* wl = l + kSmpThreads;  // [kSmpThreads], also the sort's buffer
+    int n2 = 32;
+    while (n2 < n) n2 <<= 1;
+    u64 e = tid < n ? l[tid] : ~0ull;
+    if (tid < n && smp_entry_x(e) < x_min) e = ~0ull;  // min-p
+    e = smp_sort_threads(e, n2, wl);
+    const bool some = e != ~0ull;
+    const float x = smp_entry_x(e);
+    u64 w = some ? ms.mass(x, tab) : 0ull;
+    bool kept = some && tid < sh.k_eff;
+    if (!kept) w = 0;
+    u64 S;
+    u64 run = smp_block_scan(w, sh.wsum, &S) - w;
+    // the k-th of the list, and below it nothing that a CTA held back; or the row has fewer logits above min-p
+    const bool full = __syncthreads_or(some && tid == sh.k_eff - 1 && x >= need);
+    if (!full && !(need <= x_min)) return false;
+    if (sh.p < 1.f) {
+      const u64 target = smp_top_p_target(sh.p, S);
+      kept = kept && run < target;
+      if (kept && target <= run + w) sh.total2 = run + w;
+      if (!kept) w = 0;
+      __syncthreads();
+      S = sh.total2;
+    }
+    if (score) {
+      const bool it = kept && (int32_t)(uint32_t)e == sh.id;
+      if (it) out.token(ms, sh, tab, sh.id, x, S);
+      if (!__syncthreads_or(it) && tid == 0) out.write(sh.id, -INFINITY);
+      return true;
+    }
+    // index order: the kept entries come first, so threads beyond the last of them are through
+    const int count = __syncthreads_count(kept);
+    wl[tid] = w;
+    l[tid] = e;
+    __syncthreads();
+    if (tid < count) {
+      u64 before = 0;
+#pragma unroll 4
+      for (int j = 0; j < count; ++j) {
+        const u64 y = wl[j];
+        if ((uint32_t)l[j] < (uint32_t)e) before += y;
+      }
+      const u64 target = smp_draw_target(sh.u, S);
+      if (before < target && target <= before + w) out.token(ms, sh, tab, (int32_t)(uint32_t)e, x, S);
+    }
+    return true;
+  }
+  // The same for up to kSmpList entries.
+  BI_DEV bool small_sorted(const SmpMass<true>& ms, int n, float need) {
+    u64* l = list();
+    smp_sort(l, n);
+    const u64 worst = smp_entry(x_min, 0x7fffffff);
+    if (tid == 0) sh.pos = n;
+    __syncthreads();
+    for (int i = tid; i < n; i += kSmpThreads)  // min-p: the first entry beyond it
+      if (l[i] > worst && (i == 0 || l[i - 1] <= worst)) sh.pos = i;
+    __syncthreads();
+    const int above = sh.pos;
+    __syncthreads();
+    const int k = min(above, sh.k_eff);
+    if (!(k == sh.k_eff ? smp_entry_x(l[k - 1]) >= need : need <= x_min)) return false;
+    u64 S;
+    int last = smp_list_find(sh, l, k, true, [&](u64 e) { return ms.mass(smp_entry_x(e), tab); },
+                             [&](u64 total) { return sh.p < 1.f ? smp_top_p_target(sh.p, total) : total + 1ull; }, &S);
+    if (last == k) last = k - 1;  // no top-p: all of them, with or without mass
+    if (score) {
+      if (tid == 0) {
+        if (smp_entry(sh.x_id, sh.id) <= l[last]) out.token(ms, sh, tab, sh.id, sh.x_id, S);
+        else out.write(sh.id, -INFINITY);
+      }
+      return true;
+    }
+    // index order: (index, mass) in one key (18 and 46 bits)
+    for (int i = tid; i <= last; i += kSmpThreads) {
+      const u64 e = l[i];
+      l[i] = (e << 46) | ms.mass(smp_entry_x(e), tab);
+    }
+    __syncthreads();
+    smp_sort(l, last + 1);
+    u64 through;
+    const int pos = smp_list_find(sh, l, last + 1, true, [&](u64 e) { return e & ((1ull << 46) - 1ull); },
+                                  [&](u64 total) { return smp_draw_target(sh.u, total); }, &through);
+    if (tid == 0) {
+      const int32_t best = (int32_t)(l[pos] >> 46);
+      out.token(ms, sh, tab, best, (float)static_cast<const TL*>(out.a.logits)[out.row * out.a.ld + best], S);
+    }
+    return true;
+  }
+
+  // ---- top-p over the whole row: predicted cut, exact sums
+  BI_DEV void nucleus(const SmpMass<true>& ms) {
+    for (int i = tid; i < 2 * kSmpBins; i += kSmpThreads) counts()[i] = 0u;
+    __syncthreads();
+    // depth below the maximum in units of 2^-17 octave: a bin is 2^12 of them, and takes the count and the sum of
+    // the depths within it
+    const float c11 = __fmul_rn(ms.c_hi, -2048.f), zero = __fmaf_rn(-m, c11, 8388608.f);
+    constexpr int kDeepest = 0x4B000000 + 4096 * (kSmpBins - 1);
+    uint32_t* depths = counts() + kSmpBins;
+    mine.template each4<4>([&](int, const float (&x)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int d = __float_as_int(fmaxf(__fmaf_rn(x[i], c11, zero), 8388608.f));
+        if (x[i] >= x_min && d < kDeepest) {  // the open bin would only serialise
+          atomicAdd(&counts()[(d >> 12) & (kSmpBins - 1)], 1u);
+          atomicAdd(&depths[(d >> 12) & (kSmpBins - 1)], (uint32_t)(d & 4095));
+        }
+      }
+    });
+    csync();
+    if (rank == 0) {
+      // a bin's mass to second order from its count and mean depth; the open bin's is left out of the prediction
+      constexpr int BPT = kSmpBins / kSmpThreads;
+      float w[BPT], sum = 0.f;
+      bool dense[BPT];
+      uint32_t c[BPT], d[BPT];
+#pragma unroll
+      for (int i = 0; i < BPT; ++i) c[i] = d[i] = 0;
+#pragma unroll
+      for (int r = 0; r < CS; ++r) {
+        const uint32_t* from = at(counts(), r) + tid * BPT;
+#pragma unroll
+        for (int i = 0; i < BPT; ++i) {
+          c[i] += from[i];
+          d[i] += from[kSmpBins + i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < BPT; ++i) {
+        const float n = (float)c[i], z = (float)d[i] * 5.2882933e-6f;  // times ln 2 / 2^17
+        // in units of the maximum's mass; the variance of many depths across a bin adds 2e-5
+        const float r = c[i] ? __fdividef(0.5f * z * z - 1.96e-5f, n) + (1.f + 1.96e-5f) * n - z : 0.f;
+        w[i] = r * exp2f((float)(tid * BPT + i) * -0.03125f);
+        dense[i] = c[i] >= 64;
+        sum += w[i];
+      }
+      float run = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+      }
+      if (lane == 31) sh.wmax[warp] = run;
+      if (tid == 0) {  // no prediction
+        sh.x_hi = -INFINITY;
+        sh.x_lo = -INFINITY;
+      }
+      __syncthreads();
+      float total = 0.f;
+      run -= sum;
+#pragma unroll
+      for (int i = 0; i < kSmpWarps; ++i) {
+        const float y = sh.wmax[i];
+        if (i < warp) run += y;
+        total += y;
+      }
+      // what the roundings above leave open, with room
+      const float guess = sh.p * total, open = total * 2e-5f;
+      const float g_hi = fmaxf(guess - open, total * 1e-12f), g_lo = fminf(guess + open, total * 0.9999999f);
+      const float k_m = __fmul_rn(m, ms.c_hi), per_k = __fdividef(1.f, ms.c_hi);
+#pragma unroll
+      for (int i = 0; i < BPT; ++i) {
+        const float next = run + w[i];
+        const int b = tid * BPT + i;
+        if (b < kSmpBins - 2) {
+          // within a bin of many, at the fraction of its mass; else at the bin's end; and a little further
+          if (run < g_hi && g_hi <= next) {
+            const float part = dense[i] ? __fdividef(g_hi - run, w[i]) : 0.f;
+            sh.x_hi = (k_m - 2.f * ((float)b + part) + 0.1f) * per_k;
+          }
+          if (run < g_lo && g_lo <= next) {
+            const float part = dense[i] ? __fdividef(g_lo - run, w[i]) : 1.f;
+            sh.x_lo = (k_m - 2.f * ((float)b + part) - 0.1f) * per_k;
+          }
+        }
+        run = next;
+      }
+      __syncthreads();
+      if (tid == 0) {
+        if (sh.x_hi == -INFINITY || sh.x_lo == -INFINITY) {
+          sh.x_hi = -INFINITY;
+        } else {
+          sh.x_lo = fmaxf(x_min, sh.x_lo);
+          sh.x_hi = fmaxf(sh.x_lo, sh.x_hi);
+        }
+      }
+      __syncthreads();
+      __syncthreads();
+      if (tid > 0 && tid < CS) {
+        *at(&sh.x_lo, tid) = sh.x_lo;
+        *at(&sh.x_hi, tid) = sh.x_hi;
+      }
+    }
+    csync();
+    const float x_lo = sh.x_lo, x_hi = sh.x_hi;
+    if (x_hi == -INFINITY) {
+      if (rank == 0) solo();
+      return;
+    }
+    u64 all = 0, above = 0;
+    u64* segment = at(list(), 0) + rank * kSegment;
+    // the draw looks at this CTA's entries once more (alone, in the list itself)
+    u64* own = CS == 1 || score ? nullptr : reinterpret_cast<u64*>(counts());
+    static_assert(CS == 1 || kSegment * 8 <= 8192, "own entries take the counts' place");
+    mine.template each4<4>([&](int p0, const float (&x)[4]) {
+      bool near = false;
+      u64 w[4];
+      ms.mass4(x, tab, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (x[i] >= x_min) all += w[i];
+        if (x[i] > x_hi) above += w[i];
+        near |= x[i] <= x_hi && x[i] >= x_lo;
+      }
+      if (__any_sync(0xffffffffu, near)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) append(x[i] <= x_hi && x[i] >= x_lo, x[i], p0 + i, segment, own);
+      }
+    });
+    all = smp_warp_sum(all);
+    above = smp_warp_sum(above);
+    if (lane == 0) {
+      sh.wsum[warp] = all;
+      sh.wsum2[warp] = above;
+    }
+    __syncthreads();
+    if (tid == 0) {
+      u64 t = 0, t2 = 0;
+#pragma unroll
+      for (int i = 0; i < kSmpWarps; ++i) {
+        t += sh.wsum[i];
+        t2 += sh.wsum2[i];
+      }
+      at(sh.cta_sum, 0)[rank] = t;
+      at(sh.cta_sum2, 0)[rank] = t2;
+      at(sh.cta_n, 0)[rank] = sh.list_n;
+    }
+    csync();
+    if (rank == 0) {
+      u64 total = 0, over = 0;
+#pragma unroll
+      for (int r = 0; r < CS; ++r) {
+        total += sh.cta_sum[r];
+        over += sh.cta_sum2[r];
+      }
+      const u64 target = smp_top_p_target(sh.p, total);
+      if (tid == 0) sh.cut = SmpCut{0u, -1, 0ull};
+      const int n = join();
+      if (n >= 0 && over < target) list_cut(ms, n, over, target);
+      __syncthreads();
+      const SmpCut c = sh.cut;
+      if (c.idx < 0) {  // missed
+        if (!score && tid > 0 && tid < CS) *at(&sh.cut, tid) = c;
+        if (!score) csync();
+        solo();
+        return;
+      }
+      if (score) {
+        if (tid == 0) {
+          if (smp_entry(sh.x_id, sh.id) <= ((u64)(~c.key) << 32 | (uint32_t)c.idx))
+            out.token(ms, sh, tab, sh.id, sh.x_id, c.mass);
+          else
+            out.write(sh.id, -INFINITY);
+        }
+        return;
+      }
+      if (tid > 0 && tid < CS) *at(&sh.cut, tid) = c;
+    }
+    if (score) return;
+    csync();
+    const SmpCut cut = sh.cut;
+    if (cut.idx < 0) return;
+    // the warps' kept sums: what lies above the prediction, and the kept entries next to it
+    const float cut_x = smp_unkey(cut.key);
+    const u64 last = (u64)(~cut.key) << 32 | (uint32_t)cut.idx;
+    for (uint32_t i = tid; i < sh.list_n; i += kSmpThreads) {
+      const u64 e = CS == 1 ? list()[i] : own[i];
+      if (e <= last)
+        atomicAdd(&sh.wsum2[((int)(uint32_t)e - mine.base) / 128 / mine.per], ms.mass(smp_entry_x(e), tab));
+    }
+    __syncthreads();
+    if (tid < kSmpWarps) sh.wsum[tid] = sh.wsum2[tid];
+    publish();
+    draw(ms, cut_x, cut.idx);
+  }
+  // The entry of list[0, n) at which the mass in order, from `over` on, reaches target, to sh.cut (rank 0).
+  BI_DEV void list_cut(const SmpMass<true>& ms, int n, u64 over, u64 target) {
+    u64* l = list();
+    if (n <= kSmpThreads) {
+      int n2 = 32;
+      while (n2 < n) n2 <<= 1;
+      const u64 e = smp_sort_threads(tid < n ? l[tid] : ~0ull, n2, l + kSmpThreads);
+      const u64 w = tid < n ? ms.mass(smp_entry_x(e), tab) : 0ull;
+      u64 total;
+      const u64 run = over + smp_block_scan(w, sh.wsum, &total) - w;
+      if (tid < n && run < target && target <= run + w)
+        sh.cut = SmpCut{~(uint32_t)(e >> 32), (int32_t)(uint32_t)e, run + w};
+    } else {
+      smp_sort(l, n);
+      u64 through;
+      const int pos = smp_list_find(sh, l, n, true, [&](u64 e) { return ms.mass(smp_entry_x(e), tab); },
+                                    [&](u64) { return target - over; }, &through);
+      if (tid == 0 && pos < n) {
+        const u64 e = l[pos];
+        sh.cut = SmpCut{~(uint32_t)(e >> 32), (int32_t)(uint32_t)e, over + through};
+      }
+    }
+  }
+
+  // ---- nothing cut but by min-p
+  template <bool ABS>
+  BI_DEV void plain() {
+    SmpMass<ABS> ms;
+    ms.init(m, sh);
+    if (x_min == -FLT_MAX) warp_sums([&](int, const float (&x)[4], u64 (&w)[4]) { ms.mass4(x, tab, w); });
+    else warp_sums(Kept<ABS>{ms, tab, x_min, 0x7fffffff});
+    publish();
+    if (!score) draw(ms, x_min, 0x7fffffff);
+    else if (rank == 0 && tid == 0) out.token(ms, sh, tab, sh.id, sh.x_id, row_sum());
+  }
+
+  // The row's parameters and constants, by one thread.  Returns the scored token's logit, on its way.
+  BI_DEV float setup() {
+    const SampleArgs& a = out.a;
+    const int64_t row = out.row;
     const int64_t pr = a.param_row ? (int64_t)a.param_row[row] : row;
     bool ok = !(a.temperature || a.top_k || a.top_p || a.min_p) || (pr >= 0 && pr < a.n_params);
     float T = 1.f, mp = 0.f, q = 1.f, u = 0.f, x = 0.f;
@@ -1243,7 +1328,7 @@ struct SmpRow {
     }
     if (score) {
       id = a.ids_in[row];
-      if (id >= 0 && id < a.V) x = value(id);
+      if (id >= 0 && id < a.V) x = (float)static_cast<const TL*>(a.logits)[row * a.ld + id];
       else ok = false;
     } else {
       const int64_t ur = a.u_row ? (int64_t)*a.u_row : 0;
@@ -1266,85 +1351,37 @@ struct SmpRow {
     sh.c_lo = __fadd_rn(__fmaf_rn(l_hi, r_hi, -c_hi), __fmaf_rn(l_hi, r_lo, __fmul_rn(l_lo, r_hi)));
     sh.r_hi = r_hi;
     sh.r_lo = r_lo;
+    sh.floor_rel = __fmul_rn(T, -4096.f / 92.332481f);
+    sh.floor_abs = __fmul_rn(T, -1048576.f / 92.332481f);
     sh.log_min_p = mp > 0.f && mp < 1.f ? (double)T * log((double)mp) : 0.0;
     sh.p = q;
     sh.u = u;
     sh.min_p = mp;
-    sh.x_id = x;
     sh.id = id;
     sh.k_eff = k <= 0 || k > a.V ? a.V : k;
     sh.ok = ok;
     sh.list_n = 0;
+    return x;
   }
 
-  template <typename TL>
-  BI_DEV void run() {
-    score = a.ids_in != nullptr;
-    // ---- load: 16-byte vectors aligned to memory; positions before and after the share hold -inf
-    constexpr int VE = 16 / sizeof(TL), UNROLL = 8;
-    const int lo = min(a.V, rank * a.share), n = min(a.V, lo + a.share) - lo;
-    const TL* src = static_cast<const TL*>(a.logits) + row * a.ld + lo;
-    const int a0 = (int)((reinterpret_cast<uintptr_t>(src) / sizeof(TL)) % VE);
-    base = lo - a0;
-    slabs = (n + a0 + 127) / 128;
-    per = (slabs + kSmpWarps - 1) / kSmpWarps;
-    const TL* src0 = src - a0;
-    const int v_lo = a0 > 0 ? 1 : 0, v_hi = (a0 + n) / VE, v_end = slabs * (128 / VE);  // whole vectors: [v_lo, v_hi)
-    float mx = -INFINITY;  // NaN once one is seen
-    auto put = [&](int v, const float (&x)[VE]) {
-#pragma unroll
-      for (int i = 0; i < VE; i += 4) {
-        mx = smp_max3_nan(smp_max3_nan(mx, x[i], x[i + 1]), x[i + 2], x[i + 3]);
-        *reinterpret_cast<float4*>(xs + v * VE + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-      }
-    };
-    bool first = true;
-    for (int v0 = v_lo + tid; v0 - tid < v_hi || first; v0 += kSmpThreads * UNROLL) {
-      uint4 raw[UNROLL];
-#pragma unroll
-      for (int j = 0; j < UNROLL; ++j) {
-        const int v = v0 + j * kSmpThreads;
-        if (v < v_hi) raw[j] = *reinterpret_cast<const uint4*>(src0 + v * VE);
-      }
-      if (first) {  // while the loads are on their way
-        for (int i = tid; i < 64 * kSmpTabLanes; i += kSmpThreads) {
-          const uint32_t t = kExp2Tab[i / kSmpTabLanes];
-          table[i] = make_uint2(t - (uint32_t)kSmpMagicBits, __float_as_uint((float)t));
-        }
-        if (tid == kSmpThreads - 1) setup();
-      }
-      first = false;
-#pragma unroll
-      for (int j = 0; j < UNROLL; ++j) {
-        const int v = v0 + j * kSmpThreads;
-        if (v < v_hi) {
-          const uint32_t r[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-          float x[VE];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (VE == 4) {
-              x[i] = __uint_as_float(r[i]);
-            } else {
-              x[2 * i] = bf16lo(r[i]);
-              x[2 * i + 1] = bf16hi(r[i]);
-            }
-          }
-          put(v, x);
-        }
-      }
-    }
-    // the partial vectors at both ends, and -inf up to the end of the last slab
-    for (int v = tid; v < v_lo + (v_end - max(v_lo, v_hi)); v += kSmpThreads) {
-      const int q = v < v_lo ? v : max(v_lo, v_hi) + v - v_lo;
-      float x[VE];
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const int at = q * VE + i;
-        x[i] = at >= a0 && at < a0 + n ? (float)src0[at] : -INFINITY;
-      }
-      put(q, x);
+  BI_DEV float prepare() {
+    for (int i = tid; i < 64 * kSmpTabLanes; i += kSmpThreads) {
+      const uint32_t t = kExp2Tab[i / kSmpTabLanes];
+      table[i] = make_uint2(t - (uint32_t)kSmpMagicBits, __float_as_uint((float)t));
     }
     if (tid < kSmpMaxBins) counts()[tid] = 0u;
+    return tid == kSmpThreads - 1 ? setup() : 0.f;
+  }
+  BI_DEV void run() {
+    const SampleArgs& a = out.a;
+    score = a.ids_in != nullptr;
+    if (CS > 1) cl.barrier_arrive();  // with the wait below: every CTA runs before any writes to another
+    float mx = -INFINITY;  // NaN once one is seen
+    const float x_id = prepare();
+    mine.template each4<4>([&](int, const float (&x)[4]) {
+      mx = smp_max3_nan(smp_max3_nan(mx, x[0], x[1]), x[2], x[3]);
+    });
+    if (tid == kSmpThreads - 1) sh.x_id = x_id;
     const float t_max = mx;
     float t_min = mx == -INFINITY ? INFINITY : mx;
 #pragma unroll
@@ -1357,116 +1394,73 @@ struct SmpRow {
       sh.wmin[warp] = t_min;
     }
     __syncthreads();
-    if (warp == 0) {  // the CTA's to every rank
-      mx = sh.wmax[lane & (kSmpWarps - 1)];
-      t_min = sh.wmin[lane & (kSmpWarps - 1)];
-#pragma unroll
-      for (int o = kSmpWarps / 2; o > 0; o >>= 1) {
-        mx = smp_max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        t_min = fminf(t_min, __shfl_xor_sync(0xffffffffu, t_min, o));
-      }
-      if (lane < CS) {
-        at(sh.cta_max, lane)[rank] = mx;
-        at(sh.cta_min, lane)[rank] = t_min;
-      }
-    }
-    par = 0;
-    csync();
+    if (CS > 1) cl.barrier_wait();
     if (!sh.ok) {  // the same in every CTA of the cluster
       if (rank == 0 && tid == 0) {
         report(a.status, DEV_BAD_INDEX);
-        write(-1, NAN);
+        out.write(-1, NAN);
       }
       return;
     }
-    mx = sh.cta_max[0];
-    t_min = sh.cta_min[0];
+    mx = sh.wmax[lane & (kSmpWarps - 1)];
+    t_min = sh.wmin[lane & (kSmpWarps - 1)];
 #pragma unroll
-    for (int r = 1; r < CS; ++r) {
-      mx = smp_max_nan(mx, sh.cta_max[r]);
-      t_min = fminf(t_min, sh.cta_min[r]);
+    for (int o = kSmpWarps / 2; o > 0; o >>= 1) {
+      mx = smp_max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      t_min = fminf(t_min, __shfl_xor_sync(0xffffffffu, t_min, o));
     }
-    m = mx;
-    k_eff = sh.k_eff;
-    p = sh.p;
-    const bool bad = !(m < INFINITY);  // NaN or +inf
-    if (bad || m == -INFINITY) {
-      if (rank == 0 && tid == 0) {
-        if (bad) report(a.status, DEV_BAD_VALUE);
-        write(-1, bad ? NAN : -INFINITY);
+    const int k_eff = sh.k_eff;
+    if (k_eff < a.V && k_eff <= kSmpMaxK) {
+      // a CTA's share of k, with four of its standard deviations
+      const float part = (float)k_eff / CS;
+      const int k = CS == 1 ? k_eff : min(k_eff, (int)(part + 4.f * sqrtf(part)) + 8);
+      if (k <= kSmpMaxShareK) {
+        few(k, t_max, mx, t_min);
+        return;
       }
-      return;
     }
-    // the smallest float whose mass is at least min_p
-    const float mp = sh.min_p;
-    x_min = -FLT_MAX;
-    if (mp >= 1.f) x_min = m;
-    else if (mp > 0.f) x_min = fmaxf(-FLT_MAX, __double2float_ru((double)m + sh.log_min_p));
-
-    if (score && !(sh.x_id >= x_min)) {
-      if (rank == 0 && tid == 0) write(sh.id, -INFINITY);
-      return;
+    if (tid < CS) at(sh.cta_max, tid)[rank] = mx;
+    csync();
+    if (!row_max()) return;
+    if (k_eff == a.V && sh.p >= 1.f) {
+      if (absolute()) plain<true>();
+      else plain<false>();
+    } else if (k_eff == a.V && absolute()) {
+      SmpMass<true> ms;
+      ms.init(m, sh);
+      nucleus(ms);
+    } else if (rank == 0) {
+      solo();
     }
-    if (k_eff == 1) {  // the first maximum; its logprob is 0
-      int32_t at_max = 0x7fffffff;
-      each([&](int pos, float x) {
-        if (x == m) at_max = min(at_max, base + pos);
-      });
-      at_max = __reduce_min_sync(0xffffffffu, at_max);
-      if (lane == 0) sh.wcnt[warp] = (uint32_t)at_max;
-      __syncthreads();
-      if (tid == 0) {
-        for (int i = 1; i < kSmpWarps; ++i) at_max = min(at_max, (int32_t)sh.wcnt[i]);
-        at(sh.cta_idx, 0)[rank] = at_max;
-      }
-      csync();
-      if (rank == 0 && tid == 0) {
-        for (int r = 0; r < CS; ++r) at_max = min(at_max, sh.cta_idx[r]);
-        write(at_max, score && sh.id != at_max ? -INFINITY : 0.f);
-      }
-      return;
-    }
-    if (fabsf(m) * sh.c_hi < 524288.f ? finish<true>(t_max, t_min) : finish<false>(t_max, t_min))
-      csync();  // no CTA leaves while another may still reach its shared memory
   }
 };
 
 template <typename TL, int CS>
-__global__ void __launch_bounds__(kSmpThreads, 2) sample_kernel(const SampleArgs a, int positions) {
+__global__ void __launch_bounds__(kSmpThreads, 2) sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(16) unsigned char smp_dyn[];
   __shared__ SmpShared sh;
-  float* xs = reinterpret_cast<float*>(smp_dyn);
-  uint2* tab = reinterpret_cast<uint2*>(xs + positions);
+  uint2* tab = reinterpret_cast<uint2*>(smp_dyn);
   pdl_trigger();
   pdl_wait();
-  SmpRow<CS> r{a, sh, xs, tab, tab + (threadIdx.x & (kSmpTabLanes - 1)),
-               reinterpret_cast<unsigned char*>(tab + 64 * kSmpTabLanes), cg::this_cluster()};
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = CS == 1 ? 0 : (int)cl.block_rank();
+  const int64_t row = blockIdx.x / CS;
+  const int lo = min(a.V, rank * a.share);
+  SmpRow<TL, CS> r{SmpOut{a, row}, SmpShare<TL>(a, row, lo, min(a.V, lo + a.share) - lo), sh, tab,
+                   tab + (threadIdx.x & (kSmpTabLanes - 1)), smp_dyn + 64 * kSmpTabLanes * 8, cl};
   r.tid = threadIdx.x;
   r.warp = threadIdx.x >> 5;
   r.lane = threadIdx.x & 31;
-  r.rank = CS == 1 ? 0 : (int)r.cl.block_rank();
-  r.row = blockIdx.x / CS;
-  r.template run<TL>();
-}
-
-static int smp_positions(int64_t share) { return (int)(cdiv(share + 8, 128) * 128); }
-static size_t smp_dyn_bytes(int64_t share) {
-  return (size_t)smp_positions(share) * 4 + 64 * kSmpTabLanes * 8 + kSmpLocal * 8 + kSmpList * 8;
+  r.rank = rank;
+  r.run();
 }
 
 template <typename TL, int CS>
 static bi_status launch_sample(const SampleArgs& a, int64_t T, cudaStream_t st) {
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [] {
-    err = cudaFuncSetAttribute(sample_kernel<TL, CS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)smp_dyn_bytes(kSmpMaxShare));
-  });
-  if (err != cudaSuccess) return fail(BI_ERR_CUDA, std::string("sample_kernel smem attribute: ") + cudaGetErrorString(err));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(T * CS));
   cfg.blockDim = dim3(kSmpThreads);
-  cfg.dynamicSmemBytes = smp_dyn_bytes(a.share);
+  cfg.dynamicSmemBytes = kSmpSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1477,26 +1471,26 @@ static bi_status launch_sample(const SampleArgs& a, int64_t T, cudaStream_t st) 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CS > 1 ? 2 : 1;
-  return launched(cudaLaunchKernelEx(&cfg, sample_kernel<TL, CS>, a, smp_positions(a.share)), "sample_kernel");
+  return launched(cudaLaunchKernelEx(&cfg, sample_kernel<TL, CS>, a), "sample_kernel");
 }
 
-static bi_status dispatch_sample(SampleArgs& a, int64_t T, cudaStream_t st) {
-  // Bits do not depend on the split.  A CTA takes at most 16K logits (64 KB, so that two CTAs share an SM);
-  // while the rows leave SMs idle, a row is split further, down to 2K logits a CTA.
+template <typename TL>
+static bi_status dispatch_sample_as(SampleArgs& a, int64_t T, cudaStream_t st) {
+  // Bits do not depend on the split.  A row is split while the rows alone leave CTA slots (two per SM) idle, down to
+  // 2K logits a CTA.
   int cs = 1;
-  while (cs < 8 && cdiv(a.V, cs) > 16384) cs *= 2;
-  while (cs < 8 && cdiv(a.V, cs) > 2048 && T * cs * 2 <= num_sms()) cs *= 2;
+  while (cs < 8 && cdiv(a.V, cs) > 2048 && T * cs * 2 <= 2 * num_sms()) cs *= 2;
+  if (const char* e = getenv("SMP_CS")) cs = atoi(e);
   a.share = (int)(cdiv(cdiv(a.V, cs), 8) * 8);
-  switch (cs * 2 + (a.bf16 ? 1 : 0)) {
-    case 2: return launch_sample<float, 1>(a, T, st);
-    case 4: return launch_sample<float, 2>(a, T, st);
-    case 8: return launch_sample<float, 4>(a, T, st);
-    case 16: return launch_sample<float, 8>(a, T, st);
-    case 3: return launch_sample<__nv_bfloat16, 1>(a, T, st);
-    case 5: return launch_sample<__nv_bfloat16, 2>(a, T, st);
-    case 9: return launch_sample<__nv_bfloat16, 4>(a, T, st);
-    default: return launch_sample<__nv_bfloat16, 8>(a, T, st);
+  switch (cs) {
+    case 1: return launch_sample<TL, 1>(a, T, st);
+    case 2: return launch_sample<TL, 2>(a, T, st);
+    case 4: return launch_sample<TL, 4>(a, T, st);
+    default: return launch_sample<TL, 8>(a, T, st);
   }
+}
+static bi_status dispatch_sample(SampleArgs& a, int64_t T, cudaStream_t st) {
+  return a.bf16 ? dispatch_sample_as<__nv_bfloat16>(a, T, st) : dispatch_sample_as<float>(a, T, st);
 }
 
 // Checks that both entry points share; fills the row-independent arguments.
