@@ -13,7 +13,7 @@
 // A token choice sits next to a border of a running sum: a relative error e of the masses moves
 // the choice in about 2 e sqrt(N) of the rows over N tokens of like mass, so fp32 masses (6e-8)
 // would change one row in 25,000 at N = 1e5, and top-p cuts likewise.  The masses are therefore
-// fixed-point integers of about 2^44 for the largest: 2^(j/64) from a table (Tang's table-driven
+// fixed-point integers of about 2^56 for the largest: 2^(j/64) from a table (Tang's table-driven
 // exponential, ACM TOMS 15, 1989) times a cubic in the remainder, whose argument is reduced in two
 // floats, about 5e-10 relative.  Integer sums have no order, every quantity below is defined by
 // them alone, and so a row's bits depend neither on how many CTAs share it, nor on which of the
@@ -49,21 +49,24 @@ namespace cg = cooperative_groups;
 namespace bi {
 
 typedef unsigned long long u64;
+typedef unsigned __int128 Sum;  // of masses
 
 constexpr int kSmpThreads = 512;
 constexpr int kSmpWarps = kSmpThreads / 32;
 constexpr int kSmpBins = 1024;             // bins of top-p's counts (1/32 octave); the last one is open
 constexpr int kSmpMaxBins = 256;           // bins of the threads' maxima
-constexpr int kSmpMassBins = kSmpThreads;          // bins of a histogram with masses (count and four 12-bit limbs)
+constexpr int kSmpMassBins = kSmpThreads;          // bins of a histogram with masses (count and five 12-bit limbs)
 constexpr int kSmpMassShift = 2;           // 32 octaves of 1/64 over them
 constexpr int kSmpMassBits = 9;            // log2 of them
 constexpr int kSmpList = 2048;             // candidates that one CTA orders
 constexpr int kSmpMaxK = 1024;             // top_k up to which the kept set goes straight to the list
 constexpr int kSmpMaxShareK = kSmpThreads * 3 / 4;        // and each CTA's bound is the k'-th maximum for k' up to this
-constexpr int kSmpMaxV = 1 << 18;          // 2^18 masses below 2^44.6 sum to less than 2^63
+constexpr int kSmpMaxV = 1 << 18;
 // The table's mantissa of 1 is 380000000: about the largest for which its products with 2^(f/64) - 1 round
 // by the magic number (2 * 380000000 * (2^(1/128) - 1) is below 2^22).
-constexpr int kSmpFrac = 15;               // mass = mantissa (below 2^29.6) << 15 >> octaves below the largest
+constexpr int kSmpFrac = 27;               // mass = mantissa (below 2^29.6) << 27 >> octaves below the largest
+                                           // (a small unit: 1e5 small masses, each cut by half a unit on average,
+                                           // must not move the running sum by as much as one of them)
 constexpr int kSmpTabLanes = 16;           // table copies: 8-byte reads of a half-warp have no bank conflict
 constexpr int kSmpSmem = 64 * kSmpTabLanes * 8 + 8192 + kSmpList * 8;  // table, counts, list
 constexpr float kSmpMagic = 12582912.f;    // 1.5 * 2^23: adding it rounds to an integer in the low bits
@@ -103,12 +106,12 @@ struct SampleArgs {
 struct SmpCut {  // an element is kept iff its key is larger, or equal and its index not above idx
   uint32_t key;
   int32_t idx;   // -1: no cut was found
-  u64 mass;      // mass through the cut
+  Sum mass;      // mass through the cut
 };
 struct SmpFind { // a bin and what lies before it and in it
   int32_t bin;
   uint32_t before, inside;
-  u64 before_mass, inside_mass;
+  Sum before_mass;
 };
 
 // Static shared memory of one CTA.
@@ -121,11 +124,13 @@ struct SmpShared {
   int32_t k_eff, id, ok;
   // the warps' values
   float wmax[kSmpWarps], wmin[kSmpWarps];
-  u64 wsum[kSmpWarps], wsum2[kSmpWarps];
+  Sum wsum[kSmpWarps], wsum2[kSmpWarps];
+  uint32_t wlow[kSmpWarps];       // of sums of list entries, with whigh
+  u64 whigh[kSmpWarps];
   uint32_t wcnt[kSmpWarps];
   // written by the cluster's CTAs, each at its rank: what is needed of all of them is then at hand locally
   float cta_max[8], cta_min[8], cta_bound[8];
-  u64 cta_sum[8], cta_sum2[8];
+  Sum cta_sum[8], cta_sum2[8];
   uint32_t cta_n[8];
   float x_lo, x_hi;               // top-p's prediction
   SmpCut cut;
@@ -133,7 +138,7 @@ struct SmpShared {
   uint32_t list_n;
   float x_cut;
   SmpFind find;
-  u64 total, total2;
+  Sum total, total2;
   int32_t pos;
 };
 
@@ -155,30 +160,45 @@ BI_DEV float smp_max3_nan(float a, float b, float c) {
   return r;
 }
 
-// floor(f S) for 0 <= f < 1, exactly; *rest: whether f S is no integer.
-BI_DEV u64 smp_mul_floor(float f, u64 S, bool* rest) {
+// floor(f S) for 0 <= f < 1 and S < 2^76, exactly; *rest: whether f S is no integer.
+BI_DEV Sum smp_mul_floor(float f, Sum S, bool* rest) {
   const uint32_t b = __float_as_uint(f);
   const int ex = (int)(b >> 23);
-  const u64 mant = ex ? ((b & 0x7fffffu) | 0x800000u) : (b & 0x7fffffu);
+  const uint32_t mant = ex ? ((b & 0x7fffffu) | 0x800000u) : (b & 0x7fffffu);
   const int sh = 150 - (ex ? ex : 1);  // f = mant 2^-sh, sh >= 24
-  const u64 hi = __umul64hi(mant, S), lo = mant * S;
-  u64 q, r;
-  if (sh < 64) {
-    q = (hi << (64 - sh)) | (lo >> sh);
-    r = lo << (64 - sh);
-  } else {
-    const int s2 = sh - 64;
-    q = s2 < 64 ? hi >> s2 : 0ull;
-    r = lo | (s2 < 64 ? (s2 ? hi << (64 - s2) : 0ull) : hi);
-  }
-  *rest = r != 0ull;
+  const Sum v = S * mant;              // below 2^100
+  const Sum q = sh < 128 ? v >> sh : 0;
+  *rest = v != (sh < 128 ? q << sh : 0);
   return q;
 }
-
-template <typename T>
-BI_DEV T smp_warp_sum(T v) {
+// Sums below 2^96 between lanes
+BI_DEV Sum smp_shfl_up(Sum v, int o) {
+  const u64 l = __shfl_up_sync(0xffffffffu, (u64)v, o);
+  const uint32_t h = __shfl_up_sync(0xffffffffu, (uint32_t)(v >> 64), o);
+  return (Sum)h << 64 | l;
+}
+BI_DEV Sum smp_shfl_xor(Sum v, int o) {
+  const u64 l = __shfl_xor_sync(0xffffffffu, (u64)v, o);
+  const uint32_t h = __shfl_xor_sync(0xffffffffu, (uint32_t)(v >> 64), o);
+  return (Sum)h << 64 | l;
+}
+BI_DEV Sum smp_warp_scan(Sum v) {  // inclusive
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const Sum y = smp_shfl_up(v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+BI_DEV Sum smp_warp_total(Sum upto) {  // of an inclusive scan: the last lane's
+  const u64 l = __shfl_sync(0xffffffffu, (u64)upto, 31);
+  const uint32_t h = __shfl_sync(0xffffffffu, (uint32_t)(upto >> 64), 31);
+  return (Sum)h << 64 | l;
+}
+BI_DEV Sum smp_warp_sum(Sum v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += smp_shfl_xor(v, o);
   return v;
 }
 
@@ -188,23 +208,6 @@ BI_DEV float smp_diff(float x, float m, float* err) {
   const float b = __fsub_rn(d, x);
   *err = __fadd_rn(__fsub_rn(x, __fsub_rn(d, b)), __fsub_rn(-m, b));
   return d;
-}
-
-BI_DEV u64 smp_pair(float lo, float hi) {
-  u64 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-BI_DEV void smp_unpair(u64 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-BI_DEV u64 smp_fma2(u64 a, u64 b, u64 c) {  // two floats at once, each rounded as fma
-  u64 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-BI_DEV u64 smp_mul2(u64 a, u64 b) {
-  u64 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 
 // A row's mass function.  Both forms split 64 log2(e) x / T into an integer k and a remainder f, |f| <= 1/2
@@ -217,7 +220,8 @@ struct SmpMass {
   // 2^(f/64) - 1: the series to the third power of f ln2 / 64 (below 0.0055; the next term is 4e-11)
   static constexpr float a1 = 0.0108304247f, a2 = 5.86490496e-05f, a3 = 2.11731372e-07f;
   float m, c_hi, c_lo;
-  float floor_;  // ABS: logits below it are raised to it (-2^20 / c); else: x - m at or below it has no mass (-4096 / c)
+  float floor_;  // for k_of, ABS: logits below it are raised to it (-2^20 / c); else: x - m at or below it has no mass
+                 // (-4096 / c)
   int k_top;     // k of the maximum
   int oct_top;   // its octave
   int shift0;    // (shift0 - bits of the rounded sum) >> 6 = 32 - kSmpFrac + octaves below the top one
@@ -235,23 +239,13 @@ struct SmpMass {
     if (ABS) return __float_as_int(__fmaf_rn(fmaxf(x, floor_), c_hi, kSmpMagic)) - kSmpMagicBits;
     return __float_as_int(__fmaf_rn(fmaxf(__fsub_rn(x, m), floor_), c_hi, kSmpMagic)) - kSmpMagicBits;
   }
-  // The mass from the rounded sum (k in its low bits) and g = 2^(f/64) - 1: the table's 2^(k mod 64 / 64) and its
-  // product with g, rounded to an integer by the magic number (taken off the table's integers), then shifted by
-  // the octave: (mantissa 2^32) >> s, where a shift of 64 or more gives 0.  The last bit is set in place of what the
-  // shift drops, which leaves no bias: many small masses, each cut by half a unit on average, would move the running
-  // sum by more than one of them.
-  BI_DEV u64 scale(int q, float g, const uint2* tab) const {
-    const uint2 t = tab[(q & 63) * kSmpTabLanes];
-    const uint32_t M = t.x + (uint32_t)__float_as_int(__fmaf_rn(__uint_as_float(t.y), g, kSmpMagic));
-    u64 w;
-    const uint32_t by = (uint32_t)((shift0 - q) >> 6);
-    asm("shr.b64 %0, %1, %2;" : "=l"(w) : "l"((u64)M << 32), "r"(by));
-    return by < 64u ? w | 1ull : 0ull;
-  }
+  // x = (k + f) / c with k in the low bits of the rounded sum q.  2^(k/64) is a table entry and a shift by octaves;
+  // the entry's product with g = 2^(f/64) - 1 is rounded to an integer by the magic number (which the table's
+  // integers lack).  The mass is (mantissa 2^32) >> s; a shift of 64 or more gives 0, as it does for every logit that
+  // is too low for the rounded sum, -inf among them.
   BI_DEV u64 mass(float x, const uint2* tab) const {
     float q, f;
     if (ABS) {
-      x = fmaxf(x, floor_);
       q = __fmaf_rn(x, c_hi, kSmpMagic);
       f = __fmaf_rn(x, c_hi, __fsub_rn(kSmpMagic, q));
       f = __fmaf_rn(x, c_lo, f);
@@ -268,44 +262,27 @@ struct SmpMass {
       f = __fmaf_rn(dl, c_hi, f);
     }
     const float g = __fmul_rn(f, __fmaf_rn(f, __fmaf_rn(f, a3, a2), a1));
-    return scale(__float_as_int(q), g, tab);
-  }
-  // Four masses, the same bits: the float operations of ABS on two logits at a time.
-  BI_DEV void mass4(const float (&x)[4], const uint2* tab, u64 (&w)[4]) const {
-    if (!ABS) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = mass(x[i], tab);
-      return;
-    }
-    const u64 hi = smp_pair(c_hi, c_hi), lo = smp_pair(c_lo, c_lo), magic = smp_pair(kSmpMagic, kSmpMagic);
-    const u64 minus = smp_pair(-1.f, -1.f), b1 = smp_pair(a1, a1), b2 = smp_pair(a2, a2), b3 = smp_pair(a3, a3);
-#pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      const u64 v = smp_pair(fmaxf(x[i], floor_), fmaxf(x[i + 1], floor_));
-      const u64 q = smp_fma2(v, hi, magic);
-      u64 f = smp_fma2(v, hi, smp_fma2(q, minus, magic));
-      f = smp_fma2(v, lo, f);
-      const u64 g = smp_mul2(f, smp_fma2(f, smp_fma2(f, b3, b2), b1));
-      float q0, q1, g0, g1;
-      smp_unpair(q, q0, q1);
-      smp_unpair(g, g0, g1);
-      w[i] = scale(__float_as_int(q0), g0, tab);
-      w[i + 1] = scale(__float_as_int(q1), g1, tab);
-    }
+    const int bits = __float_as_int(q);
+    const uint2 t = tab[(bits & 63) * kSmpTabLanes];
+    const uint32_t M = t.x + (uint32_t)__float_as_int(__fmaf_rn(__uint_as_float(t.y), g, kSmpMagic));
+    u64 w;
+    asm("shr.b64 %0, %1, %2;" : "=l"(w) : "l"((u64)M << 32), "r"((shift0 - bits) >> 6));
+    return w;
   }
 };
 
 // v = (h + l) 2^e to 48 bits: h 24 bits in [2^23, 2^24), l the next 24
-BI_DEV void smp_split(u64 v, float& h, float& l, int& e) {
-  const int z = __clzll((long long)v);
-  const u64 n = v << z;
+BI_DEV void smp_split(Sum v, float& h, float& l, int& e) {
+  const bool wide = (u64)(v >> 64) != 0ull;  // below 2^96
+  const int z = wide ? __clzll((long long)(v >> 32)) : __clzll((long long)v);
+  const u64 n = (wide ? (u64)(v >> 32) : (u64)v) << z;
   h = (float)(uint32_t)(n >> 40);
   l = __fmul_rn((float)((uint32_t)(n >> 16) & 0xffffffu), 0x1p-24f);
-  e = 40 - z;
+  e = (wide ? 72 : 40) - z;
 }
 // ln of a kept token's probability: (x - m) / T - ln(S / W), W the mass of the maximum; both terms in two
 // floats until the last sum.
-BI_DEV float smp_logprob(float x, float m, float r_hi, float r_lo, u64 S, u64 W) {
+BI_DEV float smp_logprob(float x, float m, float r_hi, float r_lo, Sum S, Sum W) {
   float dl;
   const float d = smp_diff(x, m, &dl);
   const float ah = __fmul_rn(d, r_hi);
@@ -339,22 +316,29 @@ struct SmpOut {
     if (a.lp_out) a.lp_out[o] = lp;
   }
   template <bool ABS>
-  BI_DEV void token(const SmpMass<ABS>& ms, const SmpShared& sh, const uint2* tab, int32_t id, float x, u64 S) const {
+  BI_DEV void token(const SmpMass<ABS>& ms, const SmpShared& sh, const uint2* tab, int32_t id, float x, Sum S) const {
     write(id, smp_logprob(x, ms.m, sh.r_hi, sh.r_lo, S, ms.mass(ms.m, tab)));
   }
 };
 
 // ceil(p S), at least 1: the mass at which top-p stops
-BI_DEV u64 smp_top_p_target(float p, u64 S) {
-  if (!(p > 0.f)) return 1ull;
+BI_DEV Sum smp_top_p_target(float p, Sum S) {
+  if (!(p > 0.f)) return 1;
   bool rest;
-  const u64 q = smp_mul_floor(p, S, &rest);
-  return q + (rest || q == 0ull ? 1ull : 0ull);
+  const Sum q = smp_mul_floor(p, S, &rest);
+  return q + (rest || q == 0 ? 1 : 0);
 }
 // floor(u S) + 1: the running mass that the drawn token is the first to reach
-BI_DEV u64 smp_draw_target(float u, u64 S) {
+BI_DEV Sum smp_draw_target(float u, Sum S) {
   bool rest;
-  return smp_mul_floor(u, S, &rest) + 1ull;
+  return smp_mul_floor(u, S, &rest) + 1;
+}
+// ceil(a / b) of a quotient below 2^18
+BI_DEV u64 smp_div_up(Sum a, u64 b) {
+  u64 q = 0;
+  for (int i = 18; i >= 0; --i)
+    if ((Sum)(q + (1ull << i)) * b < a) q += 1ull << i;
+  return q + 1ull;
 }
 // candidates: (key descending, index ascending) as one ascending 64-bit key
 BI_DEV u64 smp_entry(float x, int32_t i) { return (u64)(~smp_key(x)) << 32 | (uint32_t)i; }
@@ -362,20 +346,16 @@ BI_DEV float smp_entry_x(u64 e) { return smp_unkey(~(uint32_t)(e >> 32)); }
 
 // ---------------------------------------------------------------- one CTA's helpers
 // Inclusive sum over the CTA's threads; *total: all of it.  wsum: a value per warp.
-BI_DEV u64 smp_block_scan(u64 w, u64* wsum, u64* total) {
+BI_DEV Sum smp_block_scan(Sum w, Sum* wsum, Sum* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const u64 y = __shfl_up_sync(0xffffffffu, w, o);
-    if (lane >= o) w += y;
-  }
+  w = smp_warp_scan(w);
   __syncthreads();
   if (lane == 31) wsum[warp] = w;
   __syncthreads();
-  u64 before = 0, all = 0;
+  Sum before = 0, all = 0;
 #pragma unroll
   for (int i = 0; i < kSmpWarps; ++i) {
-    const u64 t = wsum[i];
+    const Sum t = wsum[i];
     if (i < warp) before += t;
     all += t;
   }
@@ -427,10 +407,11 @@ BI_DEV void smp_sort(u64* l, int n) {
 // the number of entries) reaches target_of(total mass): its position (n: none) and the mass through it, to every
 // thread.
 template <typename F, typename G>
-BI_DEV int smp_list_find(SmpShared& sh, const u64* l, int n, bool by_mass, F mass_of, G target_of, u64* through) {
+BI_DEV int smp_list_find(SmpShared& sh, const u64* l, int n, bool by_mass, F mass_of, G target_of, Sum* through) {
   constexpr int EPT = kSmpList / kSmpThreads;
   const int tid = threadIdx.x;
-  u64 w[EPT], ws = 0;
+  u64 w[EPT];
+  Sum ws = 0;
 #pragma unroll
   for (int i = 0; i < EPT; ++i) {
     const int e = tid * EPT + i;
@@ -438,14 +419,14 @@ BI_DEV int smp_list_find(SmpShared& sh, const u64* l, int n, bool by_mass, F mas
     ws += w[i];
   }
   if (tid == 0) sh.pos = n;
-  u64 total;
-  u64 run = smp_block_scan(ws, sh.wsum, &total) - ws;
-  const u64 target = target_of(total);
+  Sum total;
+  Sum run = smp_block_scan(ws, sh.wsum, &total) - ws;
+  const Sum target = target_of(total);
 #pragma unroll
   for (int i = 0; i < EPT; ++i) {
     const int e = tid * EPT + i;
-    const u64 next = run + w[i];
-    if (e < n && (by_mass ? (run < target && target <= next) : (u64)(e + 1) == target)) {
+    const Sum next = run + w[i];
+    if (e < n && (by_mass ? (run < target && target <= next) : (Sum)(e + 1) == target)) {
       sh.pos = e;
       sh.total = next;
     }
@@ -501,9 +482,11 @@ struct SmpShare {
   }
   // A lane's four logits of a slab, in index order over the lanes.
   BI_DEV void slab4(int slab, float (&x)[4]) const { edge<4>(slab * 128 + lane * 4, x); }
-  // visit(first position, four logits) for this warp's slabs (converged), in any order; U vectors in flight
-  template <int U, typename F>
-  BI_DEV void each4(F visit) const {
+  // visit(first position, four logits) for this warp's slabs (converged), in any order; U vectors in flight, after
+  // which flush() is called: 8 visits at most in between
+  template <int U, typename F, typename G>
+  BI_DEV void each4(F visit, G flush) const {
+    static_assert(U * VE <= 32, "the visitors' sums of masses below 2^57 stay below 2^62");
     constexpr int STEP = 32 * VE;  // a warp's vector
     const int p1 = slab_hi(warp) * 128;
     for (int p = slab_lo(warp) * 128 + lane * VE; p - lane * VE < p1; p += STEP * U) {
@@ -527,7 +510,12 @@ struct SmpShare {
           }
         }
       }
+      flush();
     }
+  }
+  template <int U, typename F>
+  BI_DEV void each4(F visit) const {
+    each4<U>(visit, [] {});
   }
 };
 
@@ -554,52 +542,48 @@ struct SmpSolo {
   // The element, in index order, at which the running weight(index, x) reaches target_of(sum): found(index, x, sum).
   template <typename F, typename G, typename H>
   BI_DEV void locate(F weight, G target_of, H found) {
-    u64 w = 0;
+    Sum w = 0;
     each([&](int i, float x) { w += weight(i, x); });
     w = smp_warp_sum(w);
     __syncthreads();
     if (lane == 0) sh.wsum2[warp] = w;
     __syncthreads();
-    u64 b = 0, sum = 0;
+    Sum b = 0, sum = 0;
     for (int i = 0; i < kSmpWarps; ++i) {
       if (i < warp) b += sh.wsum2[i];
       sum += sh.wsum2[i];
     }
-    const u64 target = target_of(sum);
+    const Sum target = target_of(sum);
     if (b < target && target <= b + w) {  // one warp
       for (int s = all.slab_lo(warp); b < target && s < all.slabs; ++s) {
         const int i0 = all.base + s * 128 + lane * 4;
         float x[4];
         all.slab4(s, x);
-        u64 y[4], inc = 0;
+        u64 y[4];
+        Sum inc = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           y[i] = weight(i0 + i, x[i]);
           inc += y[i];
         }
-        u64 run = inc;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const u64 z = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += z;
-        }
-        run = b + inc - run;
+        const Sum upto = smp_warp_scan(inc);
+        Sum run = b + upto - inc;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (run < target && target <= run + y[i]) found(i0 + i, x[i], sum);
           run += y[i];
         }
-        b += __shfl_sync(0xffffffffu, inc, 31);
+        b += smp_warp_total(upto);
       }
     }
     __syncthreads();
   }
   // The cut at which the running count or mass (top_p: of the mass `target` that is left, 0 for all) reaches target.
-  BI_DEV SmpCut select(bool by_mass, float p, u64 target) {
-    uint32_t* h = reinterpret_cast<uint32_t*>(list);  // counts and four 12-bit limbs of the masses
+  BI_DEV SmpCut select(bool by_mass, float p, Sum target) {
+    uint32_t* h = reinterpret_cast<uint32_t*>(list);  // counts and five 12-bit limbs of the masses
     uint32_t lo = 0, hi = 0xffffffffu;  // keys of the active elements, once the bins are on keys
     int bin = -1, shift = 0, level = 0; // bins of 1/16 octave first
-    u64 before_c = 0, before_w = 0;
+    Sum before_c = 0, before_w = 0;
     while (true) {
       auto active = [&](float x) {
         if (!(x >= x_min)) return false;
@@ -609,7 +593,7 @@ struct SmpSolo {
         return k >= lo && k <= hi;
       };
       __syncthreads();
-      for (int i = tid; i < 5 * kSmpMassBins; i += kSmpThreads) h[i] = 0u;
+      for (int i = tid; i < 6 * kSmpMassBins; i += kSmpThreads) h[i] = 0u;
       __syncthreads();
       each([&](int, float x) {
         if (active(x)) {
@@ -617,25 +601,24 @@ struct SmpSolo {
           const u64 w = ms.mass(x, tab);
           atomicAdd(&h[b], 1u);
           // twelve-bit limbs: 2^18 of them sum to less than 2^30
-          atomicAdd(&h[kSmpMassBins + b], (uint32_t)w & 0xfffu);
-          atomicAdd(&h[2 * kSmpMassBins + b], (uint32_t)(w >> 12) & 0xfffu);
-          atomicAdd(&h[3 * kSmpMassBins + b], (uint32_t)(w >> 24) & 0xfffu);
-          atomicAdd(&h[4 * kSmpMassBins + b], (uint32_t)(w >> 36));
+#pragma unroll
+          for (int i = 0; i < 5; ++i) atomicAdd(&h[(i + 1) * kSmpMassBins + b], (uint32_t)(w >> (12 * i)) & 0xfffu);
         }
       });
       __syncthreads();
       static_assert(kSmpMassBins == kSmpThreads, "a bin per thread");
       const uint32_t c = h[tid];
-      const u64 w = (u64)h[kSmpMassBins + tid] + ((u64)h[2 * kSmpMassBins + tid] << 12) +
-                    ((u64)h[3 * kSmpMassBins + tid] << 24) + ((u64)h[4 * kSmpMassBins + tid] << 36);
-      u64 tot_c, tot_w;
-      const u64 ic = smp_block_scan(c, sh.wsum, &tot_c);
-      const u64 iw = smp_block_scan(w, sh.wsum, &tot_w);
+      Sum w = 0;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w += (Sum)h[(i + 1) * kSmpMassBins + tid] << (12 * i);
+      Sum tot_c, tot_w;
+      const Sum ic = smp_block_scan(c, sh.wsum, &tot_c);
+      const Sum iw = smp_block_scan(w, sh.wsum, &tot_w);
       if (level == 0 && by_mass) target = smp_top_p_target(p, target ? target : tot_w);
-      const u64 want = target - (by_mass ? before_w : before_c);
+      const Sum want = target - (by_mass ? before_w : before_c);
       if (want > (by_mass ? tot_w : tot_c)) return SmpCut{smp_key(x_min), 0x7fffffff, tot_w};  // too few: all stay
       if (by_mass ? (iw - w < want && want <= iw) : (ic - c < want && want <= ic))
-        sh.find = SmpFind{tid, (uint32_t)(ic - c), c, iw - w, w};
+        sh.find = SmpFind{tid, (uint32_t)(ic - c), c, iw - w};
       __syncthreads();
       const SmpFind f = sh.find;
       before_c += f.before;
@@ -673,14 +656,14 @@ struct SmpSolo {
         level = 2;
         shift = max(0, 32 - __clz(kmax - kmin) - kSmpMassBits);
       }
-      const u64 left = target - (by_mass ? before_w : before_c);
+      const Sum left = target - (by_mass ? before_w : before_c);
       if (lo == hi) {  // equal values: the first `need` of them by index
         const float x1 = smp_unkey(lo);
         const u64 w1 = ms.mass(x1, tab);
-        const u64 need = by_mass ? (left + w1 - 1) / w1 : left;  // a bin that mass reached has some
-        locate([&](int, float x) { return x >= x_min && x == x1 ? 1ull : 0ull; }, [&](u64) { return need; },
-               [&](int i, float, u64) { sh.pos = i; });
-        return SmpCut{lo, sh.pos, before_w + need * w1};
+        const u64 need = by_mass ? smp_div_up(left, w1) : (u64)left;  // a bin that mass reached has some
+        locate([&](int, float x) { return x >= x_min && x == x1 ? 1ull : 0ull; }, [&](Sum) { return (Sum)need; },
+               [&](int i, float, Sum) { sh.pos = i; });
+        return SmpCut{lo, sh.pos, before_w + (Sum)need * w1};
       }
       if (f.inside <= (uint32_t)kSmpList) {
         __syncthreads();
@@ -691,9 +674,9 @@ struct SmpSolo {
         });
         __syncthreads();
         smp_sort(list, (int)f.inside);
-        u64 through;
+        Sum through;
         const int pos = smp_list_find(sh, list, (int)f.inside, by_mass,
-                                      [&](u64 e) { return ms.mass(smp_entry_x(e), tab); }, [&](u64) { return left; },
+                                      [&](u64 e) { return ms.mass(smp_entry_x(e), tab); }, [&](Sum) { return left; },
                                       &through);
         const u64 e = list[pos];
         return SmpCut{~(uint32_t)(e >> 32), (int32_t)(uint32_t)e, before_w + through};
@@ -704,10 +687,10 @@ struct SmpSolo {
     tid = threadIdx.x;
     warp = tid >> 5;
     lane = tid & 31;
-    SmpCut cut{smp_key(x_min), 0x7fffffff, 0ull};
-    u64 left = 0;
+    SmpCut cut{smp_key(x_min), 0x7fffffff, 0};
+    Sum left = 0;
     if (sh.k_eff < out.a.V) {
-      cut = select(false, 1.f, (u64)sh.k_eff);
+      cut = select(false, 1.f, (Sum)sh.k_eff);
       left = cut.mass;
       __syncthreads();
     }
@@ -719,8 +702,8 @@ struct SmpSolo {
     const float cut_x = smp_unkey(cut.key);
     const int32_t id = sh.id;
     locate([&](int i, float x) { return x > cut_x || (x == cut_x && i <= cut.idx) ? ms.mass(x, tab) : 0ull; },
-           [&](u64 S) { return out.a.ids_in ? S : smp_draw_target(sh.u, S); },
-           [&](int i, float x, u64 S) {
+           [&](Sum S) { return out.a.ids_in ? S : smp_draw_target(sh.u, S); },
+           [&](int i, float x, Sum S) {
              if (!out.a.ids_in) out.token(ms, sh, tab, i, x, S);
              else sh.total2 = S;
            });
@@ -805,27 +788,33 @@ struct SmpRow {
   // Warp sums to sh.wsum; then, with publish(), the CTA's sum to every rank's sh.cta_sum.
   template <typename F>
   BI_DEV void warp_sums(F weight4) {
-    u64 sum = 0;
-    mine.template each4<4>([&](int p0, const float (&x)[4]) {
-      u64 w[4];
-      weight4(mine.base + p0, x, w);
-      sum += (w[0] + w[1]) + (w[2] + w[3]);
-    });
+    Sum sum = 0;
+    u64 some = 0;
+    mine.template each4<4>(
+        [&](int p0, const float (&x)[4]) {
+          u64 w[4];
+          weight4(mine.base + p0, x, w);
+          some += (w[0] + w[1]) + (w[2] + w[3]);
+        },
+        [&] {
+          sum += some;
+          some = 0;
+        });
     sum = smp_warp_sum(sum);
     if (lane == 0) sh.wsum[warp] = sum;
   }
   BI_DEV void publish() {
     __syncthreads();
     if (tid < CS) {
-      u64 t = 0;
+      Sum t = 0;
 #pragma unroll
       for (int i = 0; i < kSmpWarps; ++i) t += sh.wsum[i];
       at(sh.cta_sum, tid)[rank] = t;
     }
     csync();
   }
-  BI_DEV u64 row_sum() {
-    u64 t = 0;
+  BI_DEV Sum row_sum() {
+    Sum t = 0;
 #pragma unroll
     for (int r = 0; r < CS; ++r) t += sh.cta_sum[r];
     return t;
@@ -833,18 +822,18 @@ struct SmpRow {
   // After publish(): the element, in index order, at which the running weight reaches target (>= 1); the CTA that
   // holds it calls found(index, x).  Its warp's slabs are taken by a warp each.
   template <typename F, typename H>
-  BI_DEV void locate(F weight4, u64 target, H found) {
-    u64 b = 0, own = 0;
+  BI_DEV void locate(F weight4, Sum target, H found) {
+    Sum b = 0, own = 0;
 #pragma unroll
     for (int r = 0; r < CS; ++r) {
-      const u64 t = sh.cta_sum[r];
+      const Sum t = sh.cta_sum[r];
       if (r < rank) b += t;
       if (r == rank) own = t;
     }
     if (!(b < target && target <= b + own)) return;
     int unit = 0;
     for (; unit < kSmpWarps - 1; ++unit) {
-      const u64 t = sh.wsum[unit];
+      const Sum t = sh.wsum[unit];
       if (target <= b + t) break;
       b += t;
     }
@@ -858,8 +847,8 @@ struct SmpRow {
         weight4(i0, x, y);
       }
       const u64 y4 = (y[0] + y[1]) + (y[2] + y[3]);
-      u64 all;
-      u64 run = b + smp_block_scan(y4, sh.wsum2, &all) - y4;
+      Sum all;
+      Sum run = b + smp_block_scan(y4, sh.wsum2, &all) - y4;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (run < target && target <= run + y[i]) found(i0 + i, x[i]);
@@ -876,16 +865,17 @@ struct SmpRow {
     float x;
     int32_t idx;
     BI_DEV void operator()(int i0, const float (&v)[4], u64 (&w)[4]) const {
-      ms.mass4(v, tab, w);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
+        w[i] = ms.mass(v[i], tab);
         if (!(v[i] > x || (v[i] == x && i0 + i <= idx))) w[i] = 0ull;
+      }
     }
   };
   // The draw from the kept set, after publish().
   template <bool ABS>
   BI_DEV void draw(const SmpMass<ABS>& ms, float cut_x, int32_t cut_i) {
-    const u64 S = row_sum();
+    const Sum S = row_sum();
     locate(Kept<ABS>{ms, tab, cut_x, cut_i}, smp_draw_target(sh.u, S),
            [&](int i, float x) { out.token(ms, sh, tab, i, x, S); });
   }
@@ -1003,13 +993,13 @@ struct SmpRow {
     u64 w = some ? ms.mass(x, tab) : 0ull;
     bool kept = some && tid < sh.k_eff;
     if (!kept) w = 0;
-    u64 S;
-    u64 run = smp_block_scan(w, sh.wsum, &S) - w;
+    Sum S;
+    Sum run = smp_block_scan(w, sh.wsum, &S) - w;
     // the k-th of the list, and below it nothing that a CTA held back; or the row has fewer logits above min-p
     const bool full = __syncthreads_or(some && tid == sh.k_eff - 1 && x >= need);
     if (!full && !(need <= x_min)) return false;
     if (sh.p < 1.f) {
-      const u64 target = smp_top_p_target(sh.p, S);
+      const Sum target = smp_top_p_target(sh.p, S);
       kept = kept && run < target;
       if (kept && target <= run + w) sh.total2 = run + w;
       if (!kept) w = 0;
@@ -1028,13 +1018,13 @@ struct SmpRow {
     l[tid] = e;
     __syncthreads();
     if (tid < count) {
-      u64 before = 0;
+      Sum before = 0;
 #pragma unroll 4
       for (int j = 0; j < count; ++j) {
         const u64 y = wl[j];
         if ((uint32_t)l[j] < (uint32_t)e) before += y;
       }
-      const u64 target = smp_draw_target(sh.u, S);
+      const Sum target = smp_draw_target(sh.u, S);
       if (before < target && target <= before + w) out.token(ms, sh, tab, (int32_t)(uint32_t)e, x, S);
     }
     return true;
@@ -1053,9 +1043,9 @@ struct SmpRow {
     __syncthreads();
     const int k = min(above, sh.k_eff);
     if (!(k == sh.k_eff ? smp_entry_x(l[k - 1]) >= need : need <= x_min)) return false;
-    u64 S;
+    Sum S;
     int last = smp_list_find(sh, l, k, true, [&](u64 e) { return ms.mass(smp_entry_x(e), tab); },
-                             [&](u64 total) { return sh.p < 1.f ? smp_top_p_target(sh.p, total) : total + 1ull; }, &S);
+                             [&](Sum total) { return sh.p < 1.f ? smp_top_p_target(sh.p, total) : total + 1; }, &S);
     if (last == k) last = k - 1;  // no top-p: all of them, with or without mass
     if (score) {
       if (tid == 0) {
@@ -1064,19 +1054,18 @@ struct SmpRow {
       }
       return true;
     }
-    // index order: (index, mass) in one key (18 and 46 bits)
+    // index order: (index, key)
     for (int i = tid; i <= last; i += kSmpThreads) {
       const u64 e = l[i];
-      l[i] = (e << 46) | ms.mass(smp_entry_x(e), tab);
+      l[i] = (e << 32) | (uint32_t)~(uint32_t)(e >> 32);
     }
     __syncthreads();
     smp_sort(l, last + 1);
-    u64 through;
-    const int pos = smp_list_find(sh, l, last + 1, true, [&](u64 e) { return e & ((1ull << 46) - 1ull); },
-                                  [&](u64 total) { return smp_draw_target(sh.u, total); }, &through);
+    Sum through;
+    const int pos = smp_list_find(sh, l, last + 1, true, [&](u64 e) { return ms.mass(smp_unkey((uint32_t)e), tab); },
+                                  [&](Sum total) { return smp_draw_target(sh.u, total); }, &through);
     if (tid == 0) {
-      const int32_t best = (int32_t)(l[pos] >> 46);
-      out.token(ms, sh, tab, best, (float)static_cast<const TL*>(out.a.logits)[out.row * out.a.ld + best], S);
+      out.token(ms, sh, tab, (int32_t)(l[pos] >> 32), smp_unkey((uint32_t)l[pos]), S);
     }
     return true;
   }
@@ -1087,16 +1076,18 @@ struct SmpRow {
     __syncthreads();
     // depth below the maximum in units of 2^-17 octave: a bin is 2^12 of them, and takes the count and the sum of
     // the depths within it
-    const float c11 = __fmul_rn(ms.c_hi, -2048.f), zero = __fmaf_rn(-m, c11, 8388608.f);
-    constexpr int kDeepest = 0x4B000000 + 4096 * (kSmpBins - 1);
+    // (with 128 more, more than the rounding of `zero` takes off; a lower bound on the logits bounds the depths)
+    const float c11 = __fmul_rn(ms.c_hi, -2048.f), zero = __fmaf_rn(-m, c11, 8388736.f);
+    const float bottom = fminf(fmaxf(__fmaf_rn(x_min, c11, zero) - 8388608.f, 0.f) + 2.f, 4096.f * (kSmpBins - 1));
+    const uint32_t deepest = (uint32_t)bottom;
     uint32_t* depths = counts() + kSmpBins;
     mine.template each4<4>([&](int, const float (&x)[4]) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int d = __float_as_int(fmaxf(__fmaf_rn(x[i], c11, zero), 8388608.f));
-        if (x[i] >= x_min && d < kDeepest) {  // the open bin would only serialise
-          atomicAdd(&counts()[(d >> 12) & (kSmpBins - 1)], 1u);
-          atomicAdd(&depths[(d >> 12) & (kSmpBins - 1)], (uint32_t)(d & 4095));
+        const uint32_t d = (uint32_t)__float_as_int(__fmaf_rn(x[i], c11, zero)) - 0x4B000000u;
+        if (d < deepest) {  // the open bin would only serialise
+          atomicAdd(&counts()[d >> 12], 1u);
+          atomicAdd(&depths[d >> 12], d & 4095u);
         }
       }
     });
@@ -1150,7 +1141,8 @@ struct SmpRow {
       // what the roundings above leave open, with room
       const float guess = sh.p * total, open = total * 2e-5f;
       const float g_hi = fmaxf(guess - open, total * 1e-12f), g_lo = fminf(guess + open, total * 0.9999999f);
-      const float k_m = __fmul_rn(m, ms.c_hi), per_k = __fdividef(1.f, ms.c_hi);
+      const float k_m = __fmaf_rn(m, ms.c_hi, 0.0625f),  // the depths' 128 more
+                   per_k = __fdividef(1.f, ms.c_hi);
 #pragma unroll
       for (int i = 0; i < BPT; ++i) {
         const float next = run + w[i];
@@ -1190,35 +1182,43 @@ struct SmpRow {
       if (rank == 0) solo();
       return;
     }
-    u64 all = 0, above = 0;
+    Sum all = 0, above = 0;
     u64* segment = at(list(), 0) + rank * kSegment;
     // the draw looks at this CTA's entries once more (alone, in the list itself)
     u64* own = CS == 1 || score ? nullptr : reinterpret_cast<u64*>(counts());
     static_assert(CS == 1 || kSegment * 8 <= 8192, "own entries take the counts' place");
-    mine.template each4<4>([&](int p0, const float (&x)[4]) {
-      bool near = false;
-      u64 w[4];
-      ms.mass4(x, tab, w);
+    u64 some = 0, some_above = 0;
+    mine.template each4<4>(
+        [&](int p0, const float (&x)[4]) {
+          bool near = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (x[i] >= x_min) all += w[i];
-        if (x[i] > x_hi) above += w[i];
-        near |= x[i] <= x_hi && x[i] >= x_lo;
-      }
-      if (__any_sync(0xffffffffu, near)) {
+          for (int i = 0; i < 4; ++i) {
+            const u64 w = ms.mass(x[i], tab);
+            if (x[i] >= x_min) some += w;
+            if (x[i] > x_hi) some_above += w;
+            near |= x[i] <= x_hi && x[i] >= x_lo;
+          }
+          if (__any_sync(0xffffffffu, near)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) append(x[i] <= x_hi && x[i] >= x_lo, x[i], p0 + i, segment, own);
-      }
-    });
+            for (int i = 0; i < 4; ++i) append(x[i] <= x_hi && x[i] >= x_lo, x[i], p0 + i, segment, own);
+          }
+        },
+        [&] {
+          all += some;
+          above += some_above;
+          some = some_above = 0;
+        });
     all = smp_warp_sum(all);
     above = smp_warp_sum(above);
     if (lane == 0) {
       sh.wsum[warp] = all;
       sh.wsum2[warp] = above;
+      sh.wlow[warp] = 0u;
+      sh.whigh[warp] = 0ull;
     }
     __syncthreads();
     if (tid == 0) {
-      u64 t = 0, t2 = 0;
+      Sum t = 0, t2 = 0;
 #pragma unroll
       for (int i = 0; i < kSmpWarps; ++i) {
         t += sh.wsum[i];
@@ -1230,14 +1230,14 @@ struct SmpRow {
     }
     csync();
     if (rank == 0) {
-      u64 total = 0, over = 0;
+      Sum total = 0, over = 0;
 #pragma unroll
       for (int r = 0; r < CS; ++r) {
         total += sh.cta_sum[r];
         over += sh.cta_sum2[r];
       }
-      const u64 target = smp_top_p_target(sh.p, total);
-      if (tid == 0) sh.cut = SmpCut{0u, -1, 0ull};
+      const Sum target = smp_top_p_target(sh.p, total);
+      if (tid == 0) sh.cut = SmpCut{0u, -1, 0};
       const int n = join();
       if (n >= 0 && over < target) list_cut(ms, n, over, target);
       __syncthreads();
@@ -1268,31 +1268,35 @@ struct SmpRow {
     const u64 last = (u64)(~cut.key) << 32 | (uint32_t)cut.idx;
     for (uint32_t i = tid; i < sh.list_n; i += kSmpThreads) {
       const u64 e = CS == 1 ? list()[i] : own[i];
-      if (e <= last)
-        atomicAdd(&sh.wsum2[((int)(uint32_t)e - mine.base) / 128 / mine.per], ms.mass(smp_entry_x(e), tab));
+      if (e <= last) {
+        const int at_ = ((int)(uint32_t)e - mine.base) / 128 / mine.per;
+        const u64 w = ms.mass(smp_entry_x(e), tab);
+        atomicAdd(&sh.wlow[at_], (uint32_t)w & 0xfffffu);
+        atomicAdd(&sh.whigh[at_], w >> 20);
+      }
     }
     __syncthreads();
-    if (tid < kSmpWarps) sh.wsum[tid] = sh.wsum2[tid];
+    if (tid < kSmpWarps) sh.wsum[tid] = sh.wsum2[tid] + ((Sum)sh.whigh[tid] << 20) + sh.wlow[tid];
     publish();
     draw(ms, cut_x, cut.idx);
   }
   // The entry of list[0, n) at which the mass in order, from `over` on, reaches target, to sh.cut (rank 0).
-  BI_DEV void list_cut(const SmpMass<true>& ms, int n, u64 over, u64 target) {
+  BI_DEV void list_cut(const SmpMass<true>& ms, int n, Sum over, Sum target) {
     u64* l = list();
     if (n <= kSmpThreads) {
       int n2 = 32;
       while (n2 < n) n2 <<= 1;
       const u64 e = smp_sort_threads(tid < n ? l[tid] : ~0ull, n2, l + kSmpThreads);
       const u64 w = tid < n ? ms.mass(smp_entry_x(e), tab) : 0ull;
-      u64 total;
-      const u64 run = over + smp_block_scan(w, sh.wsum, &total) - w;
+      Sum total;
+      const Sum run = over + smp_block_scan(w, sh.wsum, &total) - w;
       if (tid < n && run < target && target <= run + w)
         sh.cut = SmpCut{~(uint32_t)(e >> 32), (int32_t)(uint32_t)e, run + w};
     } else {
       smp_sort(l, n);
-      u64 through;
+      Sum through;
       const int pos = smp_list_find(sh, l, n, true, [&](u64 e) { return ms.mass(smp_entry_x(e), tab); },
-                                    [&](u64) { return target - over; }, &through);
+                                    [&](Sum) { return target - over; }, &through);
       if (tid == 0 && pos < n) {
         const u64 e = l[pos];
         sh.cut = SmpCut{~(uint32_t)(e >> 32), (int32_t)(uint32_t)e, over + through};
@@ -1305,7 +1309,11 @@ struct SmpRow {
   BI_DEV void plain() {
     SmpMass<ABS> ms;
     ms.init(m, sh);
-    if (x_min == -FLT_MAX) warp_sums([&](int, const float (&x)[4], u64 (&w)[4]) { ms.mass4(x, tab, w); });
+    if (x_min == -FLT_MAX)
+      warp_sums([&](int, const float (&x)[4], u64 (&w)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = ms.mass(x[i], tab);
+      });
     else warp_sums(Kept<ABS>{ms, tab, x_min, 0x7fffffff});
     publish();
     if (!score) draw(ms, x_min, 0x7fffffff);
