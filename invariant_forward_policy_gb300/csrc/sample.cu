@@ -39,8 +39,8 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
-#include <mutex>
 #include <string>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -482,31 +482,58 @@ struct SmpShare {
   }
   // A lane's four logits of a slab, in index order over the lanes.
   BI_DEV void slab4(int slab, float (&x)[4]) const { edge<4>(slab * 128 + lane * 4, x); }
-  // visit(first position, four logits) for this warp's slabs (converged), in any order; U vectors in flight, after
-  // which flush() is called: 8 visits at most in between
+  // A lane's vectors of one batch: plain loads inside the share, logit by logit (-inf outside it) at its ends.  Returns
+  // how many of them the warp has.
+  template <int U>
+  BI_DEV int batch(int p_warp, uint4 (&raw)[U]) const {
+    constexpr int STEP = 32 * VE;  // a warp's vector
+    const int p = p_warp + lane * VE, p1 = min(p_hi, slab_hi(warp) * 128);
+    if (p_warp >= p_lo && p_warp + STEP * U <= p1) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) raw[j] = *reinterpret_cast<const uint4*>(src0 + p + j * STEP);
+      return U;
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int v = p_warp + j * STEP;
+      if (v >= p_lo && v + STEP <= p1) {
+        raw[j] = *reinterpret_cast<const uint4*>(src0 + p + j * STEP);
+      } else if (v < p1) {
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int q = p + j * STEP + i * (VE / 4);
+          if constexpr (VE == 4) {
+            r[i] = q >= p_lo && q < p1 ? reinterpret_cast<const uint32_t*>(src0)[q] : 0xff800000u;
+          } else {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(src0);
+            r[i] = (q >= p_lo && q < p1 ? h[q] : 0xff80u) | (q + 1 >= p_lo && q + 1 < p1 ? h[q + 1] : 0xff80u) << 16;
+          }
+        }
+        raw[j] = make_uint4(r[0], r[1], r[2], r[3]);
+      }
+    }
+    return min(U, (p1 - p_warp + STEP - 1) / STEP);
+  }
+  // visit(first position, four logits) for this warp's slabs (converged), in any order; a batch of U vectors at a time,
+  // after which flush() is called: 8 visits at most in between.  Positions outside the share read as -inf.
   template <int U, typename F, typename G>
   BI_DEV void each4(F visit, G flush) const {
     static_assert(U * VE <= 32, "the visitors' sums of masses below 2^57 stay below 2^62");
-    constexpr int STEP = 32 * VE;  // a warp's vector
+    constexpr int STEP = 32 * VE;
     const int p1 = slab_hi(warp) * 128;
-    for (int p = slab_lo(warp) * 128 + lane * VE; p - lane * VE < p1; p += STEP * U) {
+    for (int p = slab_lo(warp) * 128; p < p1; p += STEP * U) {
       uint4 raw[U];
+      const int n = batch<U>(p, raw);
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const int q = p + j * STEP;
-        if (q >= p_lo && q + VE <= p_hi && q < p1) raw[j] = *reinterpret_cast<const uint4*>(src0 + q);
-      }
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int q = p + j * STEP;
-        if (q - lane * VE < p1) {
+        if (j < n) {
           float x[VE];
-          if (q >= p_lo && q + VE <= p_hi) expand(raw[j], x);
-          else edge<VE>(q, x);
+          expand(raw[j], x);
 #pragma unroll
           for (int i = 0; i < VE; i += 4) {
             const float y[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
-            visit(q + i, y);
+            visit(p + lane * VE + j * STEP + i, y);
           }
         }
       }
@@ -1139,7 +1166,7 @@ struct SmpRow {
         total += y;
       }
       // what the roundings above leave open, with room
-      const float guess = sh.p * total, open = total * 2e-5f;
+      const float guess = sh.p * total, open = total * 1e-5f;
       const float g_hi = fmaxf(guess - open, total * 1e-12f), g_lo = fminf(guess + open, total * 0.9999999f);
       const float k_m = __fmaf_rn(m, ms.c_hi, 0.0625f),  // the depths' 128 more
                    per_k = __fdividef(1.f, ms.c_hi);
@@ -1148,14 +1175,16 @@ struct SmpRow {
         const float next = run + w[i];
         const int b = tid * BPT + i;
         if (b < kSmpBins - 2) {
-          // within a bin of many, at the fraction of its mass; else at the bin's end; and a little further
+          // within a bin of many, at the fraction of its mass, give or take what n places at random leave open
+          // (2.2 / sqrt(n) of a bin); else at the bin's end; and a little further
+          const float give = 0.1f + (dense[i] ? 4.4f * rsqrtf((float)c[i]) : 0.f);
           if (run < g_hi && g_hi <= next) {
             const float part = dense[i] ? __fdividef(g_hi - run, w[i]) : 0.f;
-            sh.x_hi = (k_m - 2.f * ((float)b + part) + 0.1f) * per_k;
+            sh.x_hi = (k_m - 2.f * ((float)b + part) + give) * per_k;
           }
           if (run < g_lo && g_lo <= next) {
             const float part = dense[i] ? __fdividef(g_lo - run, w[i]) : 1.f;
-            sh.x_lo = (k_m - 2.f * ((float)b + part) - 0.1f) * per_k;
+            sh.x_lo = (k_m - 2.f * ((float)b + part) - give) * per_k;
           }
         }
         run = next;
@@ -1188,26 +1217,31 @@ struct SmpRow {
     u64* own = CS == 1 || score ? nullptr : reinterpret_cast<u64*>(counts());
     static_assert(CS == 1 || kSegment * 8 <= 8192, "own entries take the counts' place");
     u64 some = 0, some_above = 0;
-    mine.template each4<4>(
-        [&](int p0, const float (&x)[4]) {
-          bool near = false;
+    const float mid = 0.5f * x_lo + 0.5f * x_hi, half = fmaxf(x_hi - mid, mid - x_lo) * 1.00001f;
+    auto pass = [&](auto with_min_p) {
+      mine.template each4<4>(
+          [&](int p0, const float (&x)[4]) {
+            float near = INFINITY;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const u64 w = ms.mass(x[i], tab);
-            if (x[i] >= x_min) some += w;
-            if (x[i] > x_hi) some_above += w;
-            near |= x[i] <= x_hi && x[i] >= x_lo;
-          }
-          if (__any_sync(0xffffffffu, near)) {
+            for (int i = 0; i < 4; ++i) {
+              const u64 w = ms.mass(x[i], tab);
+              if (!decltype(with_min_p)::value || x[i] >= x_min) some += w;
+              if (x[i] > x_hi) some_above += w;
+              near = fminf(near, fabsf(x[i] - mid));
+            }
+            if (__any_sync(0xffffffffu, near <= half)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) append(x[i] <= x_hi && x[i] >= x_lo, x[i], p0 + i, segment, own);
-          }
-        },
-        [&] {
-          all += some;
-          above += some_above;
-          some = some_above = 0;
-        });
+              for (int i = 0; i < 4; ++i) append(x[i] <= x_hi && x[i] >= x_lo, x[i], p0 + i, segment, own);
+            }
+          },
+          [&] {
+            all += some;
+            above += some_above;
+            some = some_above = 0;
+          });
+    };
+    if (x_min == -FLT_MAX) pass(std::false_type{});
+    else pass(std::true_type{});
     all = smp_warp_sum(all);
     above = smp_warp_sum(above);
     if (lane == 0) {
@@ -1488,6 +1522,8 @@ static bi_status dispatch_sample_as(SampleArgs& a, int64_t T, cudaStream_t st) {
   // 2K logits a CTA.
   int cs = 1;
   while (cs < 8 && cdiv(a.V, cs) > 2048 && T * cs * 2 <= 2 * num_sms()) cs *= 2;
+  // The rows in flight have to stay in L2 until their last pass: a row of more than 256 KB is split too.
+  if (cs == 1 && a.V * (int64_t)sizeof(TL) > 256 * 1024) cs = a.V * (int64_t)sizeof(TL) > 512 * 1024 ? 4 : 2;
   if (const char* e = getenv("SMP_CS")) cs = atoi(e);
   a.share = (int)(cdiv(cdiv(a.V, cs), 8) * 8);
   switch (cs) {
