@@ -764,6 +764,7 @@ struct SmpRow {
 
   BI_DEV uint32_t* counts() { return reinterpret_cast<uint32_t*>(area); }
   BI_DEV u64* list() { return reinterpret_cast<u64*>(area + 8192); }
+  static constexpr int kWide = 32 / SmpShare<TL>::VE;  // vectors in flight in passes that keep few registers
   static constexpr int kSegment = kSmpList / CS;  // a CTA's part of rank 0's list
 
   BI_DEV void csync() {
@@ -978,7 +979,7 @@ struct SmpRow {
     const float depth = __fmul_rn(__fdiv_rn((float)(bin + 1), scale), 1.000001f);
     const float bound = bin == kSmpMaxBins - 1 ? -FLT_MAX : fmaxf(-FLT_MAX, __fsub_rd(cta_max, depth));
     u64* segment = at(list(), 0) + rank * kSegment;
-    mine.template each4<4>([&](int p0, const float (&x)[4]) {
+    mine.template each4<kWide>([&](int p0, const float (&x)[4]) {
       const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       if (__any_sync(0xffffffffu, top >= bound)) {
 #pragma unroll
@@ -1124,24 +1125,24 @@ struct SmpRow {
       constexpr int BPT = kSmpBins / kSmpThreads;
       float w[BPT], sum = 0.f;
       bool dense[BPT];
-      uint32_t c[BPT], d[BPT];
-#pragma unroll
-      for (int i = 0; i < BPT; ++i) c[i] = d[i] = 0;
+      static_assert(BPT == 2, "a pair of bins per thread");
+      uint32_t c[BPT] = {0, 0}, d[BPT] = {0, 0};
 #pragma unroll
       for (int r = 0; r < CS; ++r) {
-        const uint32_t* from = at(counts(), r) + tid * BPT;
-#pragma unroll
-        for (int i = 0; i < BPT; ++i) {
-          c[i] += from[i];
-          d[i] += from[kSmpBins + i];
-        }
+        const uint2 v = reinterpret_cast<const uint2*>(at(counts(), r))[tid];
+        const uint2 z = reinterpret_cast<const uint2*>(at(counts(), r))[kSmpBins / BPT + tid];
+        c[0] += v.x;
+        c[1] += v.y;
+        d[0] += z.x;
+        d[1] += z.y;
       }
+      const float scale = exp2f((float)tid * -0.0625f);
 #pragma unroll
       for (int i = 0; i < BPT; ++i) {
         const float n = (float)c[i], z = (float)d[i] * 5.2882933e-6f;  // times ln 2 / 2^17
         // in units of the maximum's mass; the variance of many depths across a bin adds 2e-5
         const float r = c[i] ? __fdividef(0.5f * z * z - 1.96e-5f, n) + (1.f + 1.96e-5f) * n - z : 0.f;
-        w[i] = r * exp2f((float)(tid * BPT + i) * -0.03125f);
+        w[i] = r * (i ? scale * 0.97857206f : scale);  // 2^(-1/32)
         dense[i] = c[i] >= 64;
         sum += w[i];
       }
@@ -1198,7 +1199,6 @@ struct SmpRow {
           sh.x_hi = fmaxf(sh.x_lo, sh.x_hi);
         }
       }
-      __syncthreads();
       __syncthreads();
       if (tid > 0 && tid < CS) {
         *at(&sh.x_lo, tid) = sh.x_lo;
@@ -1420,7 +1420,7 @@ struct SmpRow {
     if (CS > 1) cl.barrier_arrive();  // with the wait below: every CTA runs before any writes to another
     float mx = -INFINITY;  // NaN once one is seen
     const float x_id = prepare();
-    mine.template each4<4>([&](int, const float (&x)[4]) {
+    mine.template each4<kWide>([&](int, const float (&x)[4]) {
       mx = smp_max3_nan(smp_max3_nan(mx, x[0], x[1]), x[2], x[3]);
     });
     if (tid == kSmpThreads - 1) sh.x_id = x_id;
@@ -1524,7 +1524,6 @@ static bi_status dispatch_sample_as(SampleArgs& a, int64_t T, cudaStream_t st) {
   while (cs < 8 && cdiv(a.V, cs) > 2048 && T * cs * 2 <= 2 * num_sms()) cs *= 2;
   // The rows in flight have to stay in L2 until their last pass: a row of more than 256 KB is split too.
   if (cs == 1 && a.V * (int64_t)sizeof(TL) > 256 * 1024) cs = a.V * (int64_t)sizeof(TL) > 512 * 1024 ? 4 : 2;
-  if (const char* e = getenv("SMP_CS")) cs = atoi(e);
   a.share = (int)(cdiv(cdiv(a.V, cs), 8) * 8);
   switch (cs) {
     case 1: return launch_sample<TL, 1>(a, T, st);
