@@ -175,7 +175,8 @@ bi_status bi_rope_table(float* rope_table, int64_t max_pos, int hd, double theta
  * alone.  A request that the pool cannot serve after the requests before it
  * (counting those that failed), or that needs more than max_blocks_per_seq
  * blocks, keeps what it has and sets the device status; n_owned_out tells
- * which.  n_owned_out [B] and pool_out [2] receive the new counts: the inputs
+ * which.  A block id outside [0, n_blocks), in the ring or in a surplus entry,
+ * is moved as it is and sets the device status.  n_owned_out [B] and pool_out [2] receive the new counts: the inputs
  * themselves, or other arrays (the table and the ring change either way).
  * lens, n_owned: device int32 [B].  extra in [0, 2^31) is added to every
  * positive length (a decode step passes its positions and extra = 1).
@@ -189,8 +190,8 @@ bi_status bi_rope_table(float* rope_table, int64_t max_pos, int hd, double theta
  * position % 64 (int64).  row_seq, row_pos and slots hold T rows and may each
  * be NULL (block_table may be, without slots).  Rows behind the last request's
  * stay as they were.  More than T rows: those beyond are left out, row0 is cut
- * at T, and the device status is set, as it is for a position without a block
- * (slot -1). */
+ * at T, and the device status is set, as it is for a position below 0 or above
+ * 2^31 - 1 or without a block (slot -1).  B = 0 writes nothing. */
 bi_status bi_block_table_resize(const int32_t* lens, int64_t extra, int64_t B, int32_t* block_table,
                                 int64_t max_blocks_per_seq, const int32_t* n_owned, int32_t* ring, int64_t n_blocks,
                                 const int32_t* pool, int32_t* n_owned_out, int32_t* pool_out, void* stream);

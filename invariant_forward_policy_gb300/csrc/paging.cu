@@ -136,13 +136,16 @@ __global__ void __launch_bounds__(kPlanThreads) block_table_resize_kernel(
       for (int i = lane; i < e.y; i += g) {  // from the ring's head on
         int64_t at = (int64_t)head + e.z + i;
         if (at >= n_blocks) at -= n_blocks;
-        row[i] = ring[at];
+        const int32_t id = ring[at];
+        if (id < 0 || id >= n_blocks) report(status, DEV_BAD_INDEX);
+        row[i] = id;
       }
       for (int i = lane; i < -e.y; i += g) {  // to its tail: never among the free ids, which are being read
         int64_t at = (int64_t)head + count + e.z + i;
         at %= n_blocks;
-        if ((int64_t)count + e.z + i < n_blocks) ring[at] = row[i];
-        else report(status, DEV_BAD_INDEX);
+        const int32_t id = row[i];
+        if ((int64_t)count + e.z + i < n_blocks) ring[at] = id;
+        if ((int64_t)count + e.z + i >= n_blocks || id < 0 || id >= n_blocks) report(status, DEV_BAD_INDEX);
         row[i] = -1;
       }
     }
@@ -241,6 +244,7 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const int32_t* __
     const int mk = mark_of[j];
     const int b = seq_of[mk] - 1;
     const int64_t pos = (int64_t)start[b] + (row - first_of[mk]);
+    if (pos < 0 || pos > 0x7fffffff) report(status, DEV_BAD_INDEX);
     if (row_seq) row_seq[row] = b;
     if (row_pos) row_pos[row] = (int32_t)pos;
     if (slots) {
@@ -289,7 +293,7 @@ bi_status bi_block_table_resize(const int32_t* lens, int64_t extra, int64_t B, i
   BI_REQUIRE(lens && block_table && n_owned && ring && pool && n_owned_out && pool_out, "null pointer");
   BI_REQUIRE(max_blocks_per_seq >= 1 && n_blocks >= 1, "max_blocks_per_seq and n_blocks must be positive");
   BI_REQUIRE(extra >= 0 && extra <= 0x7fffffff, "extra must be in [0, 2^31)");
-  BI_REQUIRE(B <= 0x7fffffff && n_blocks <= 0x7fffffff && max_blocks_per_seq <= 0x7fffffff / B,
+  BI_REQUIRE(B <= 1 << 30 && n_blocks <= 0x7fffffff && max_blocks_per_seq <= 0x7fffffff / B,
              "block table or pool too large");
   BI_REQUIRE(n_owned_out == n_owned || n_owned_out + B <= n_owned || n_owned + B <= n_owned_out,
              "n_owned_out must be n_owned or lie apart from it");
@@ -313,7 +317,7 @@ bi_status bi_slot_map(const int32_t* new_tokens, const int32_t* start, int64_t B
   BI_REQUIRE(new_tokens && start && row0, "null pointer");
   BI_REQUIRE(!slots || block_table, "slots need a block table");
   BI_REQUIRE(max_blocks_per_seq >= 1 && n_blocks >= 1, "max_blocks_per_seq and n_blocks must be positive");
-  BI_REQUIRE(B <= 0x7fffffff && n_blocks <= 0x7fffffff, "too many requests or blocks");
+  BI_REQUIRE(B <= 1 << 30 && n_blocks <= 0x7fffffff, "too many requests or blocks");
   BI_REQUIRE(T <= 0x7fffffff, "T too large");
   return launched(launch_pdl(slot_map_kernel, dim3((unsigned)std::max<int64_t>(1, cdiv(T, kMapRows))), dim3(kMapThreads), 0,
                              as_stream(stream), new_tokens, start, (int)B, block_table, max_blocks_per_seq, n_blocks, T,

@@ -157,3 +157,26 @@ def test_slots_pass_32_bits():
     bi.bi_slot_map(_i32([2]), _i32([62]), 1, _i32([[nb - 1]]), 1, nb, 2, row0, slots=slots)
     assert slots.cpu().tolist() == [(nb - 1) * 64 + 62, (nb - 1) * 64 + 63]
     assert bi.bi_device_status() == 0
+
+
+def test_bad_ids_are_moved_and_reported():
+    """The resize indexes nothing by a block id, so it only passes a bad one on, with the device status set."""
+    for bad in (-1, 10, 1 << 30):
+        pool = Pool(2, 4, 10, seed=1)
+        pool.d_ring[1] = bad
+        bi.bi_block_table_resize(_i32([64, 128]), 2, pool.d_table, 4, pool.d_owned, pool.d_ring, 10, pool.d_pool)
+        assert bi.bi_device_status() == bi.BI_ERR_DEVICE_CHECK
+        assert pool.d_owned.cpu().tolist() == [1, 2] and pool.d_table[1, 0].item() == bad
+        bi.bi_block_table_resize(_i32([64, 0]), 2, pool.d_table, 4, pool.d_owned, pool.d_ring, 10, pool.d_pool)
+        assert bi.bi_device_status() == bi.BI_ERR_DEVICE_CHECK
+        assert pool.d_owned.cpu().tolist() == [1, 0] and pool.d_pool.cpu().tolist() == [3, 9]
+
+
+def test_positions_past_31_bits_are_reported():
+    row0 = torch.zeros(2, dtype=torch.int32, device="cuda")
+    pos = torch.zeros(3, dtype=torch.int32, device="cuda")
+    bi.bi_slot_map(_i32([3]), _i32([2 ** 31 - 3]), 1, None, 1, 1, 3, row0, row_pos=pos)
+    assert pos.cpu().tolist() == [2 ** 31 - 3, 2 ** 31 - 2, 2 ** 31 - 1] and bi.bi_device_status() == 0
+    for start in (2 ** 31 - 2, -1):
+        bi.bi_slot_map(_i32([3]), _i32([start]), 1, None, 1, 1, 3, row0, row_pos=pos)
+        assert bi.bi_device_status() == bi.BI_ERR_DEVICE_CHECK
