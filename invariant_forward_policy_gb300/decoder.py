@@ -101,6 +101,8 @@ class KVPool:
     `table` [n_seq, max_blocks] is the block table of the forward calls; the free ids stand in a ring."""
 
     def __init__(self, n_seq: int, max_blocks: int, n_blocks: int, device="cuda", seed: int | None = None):
+        if min(n_seq, max_blocks, n_blocks) < 1:
+            raise ValueError("n_seq, max_blocks and n_blocks must be positive")
         self.n_seq, self.max_blocks, self.n_blocks = n_seq, max_blocks, n_blocks
         self.table = torch.full((n_seq, max_blocks), -1, dtype=torch.int32, device=device)
         self.owned = torch.zeros(n_seq, dtype=torch.int32, device=device)
@@ -108,7 +110,9 @@ class KVPool:
         self.pool = torch.tensor([0, n_blocks], dtype=torch.int32, device=device)
 
     def resize(self, lens: torch.Tensor, extra: int = 0):
-        """Blocks for lens + extra tokens of every sequence (int32 on the device; 0: all given back)."""
+        """Blocks for lens + extra tokens of every sequence (int32 [n_seq] on the device; 0: all given back)."""
+        if lens.dtype != torch.int32 or tuple(lens.shape) != (self.n_seq,) or not lens.is_contiguous():
+            raise ValueError(f"lens must be contiguous int32 [{self.n_seq}]")
         L.bi_block_table_resize(lens, self.n_seq, self.table, self.max_blocks, self.owned, self.ring, self.n_blocks,
                                 self.pool, extra=extra)
 
@@ -216,6 +220,12 @@ class Decoder:
         are drawn with `u` (fp32 [T] on the device, one per packed row)."""
         lens = [len(x) for x in seqs]
         B = len(seqs)
+        if sampling is None and u is not None:
+            raise ValueError("u without sampling")
+        if sampling is not None and (u is None) == (targets is None):
+            raise ValueError("sampling takes either targets (scored) or u (a draw)")
+        if u is not None and (tuple(u.shape) != (sum(lens),) or u.dtype != torch.float32 or not u.is_contiguous()):
+            raise ValueError(f"u must be contiguous fp32 [{sum(lens)}]")
         cu = np.zeros(B + 1, dtype=np.int64)
         cu[1:] = np.cumsum(lens)
         T = int(cu[-1])
@@ -268,6 +278,8 @@ class Decoder:
         if uniforms is not None and (tuple(uniforms.shape) != (n_gen, B) or uniforms.dtype != torch.float32
                                      or not uniforms.is_contiguous()):
             raise ValueError(f"uniforms must be contiguous fp32 [{n_gen}, {B}]")
+        if pool is not None and (pool.n_seq != B or pool.n_blocks > cache.n_blocks):
+            raise ValueError(f"the pool must be one of {B} sequences and at most {cache.n_blocks} blocks")
         lens = np.array([len(p) for p in prompts])
         max_ctx = int(lens.max()) + n_gen
         dev = self.device
@@ -327,6 +339,8 @@ class Decoder:
         the rollout's parameters; the logprobs are then those of its truncated distributions."""
         B = len(prompts)
         order = list(range(B)) if order is None else list(order)
+        if sampling is not None and any(t is not None for t in sampling.tensors) and sampling.n < B:
+            raise ValueError("fewer sampling parameters than sequences")
         gens = [np.asarray(g, np.int32) for g in gens]
         seqs, tg, lf = recompute_pack(prompts, gens, order)
         bt = block_table[torch.as_tensor(order, device=block_table.device)]

@@ -7,6 +7,7 @@ import torch
 
 import invariant_forward_policy_gb300 as bi
 from invariant_forward_policy_gb300 import _lib
+from invariant_forward_policy_gb300.decoder import Decoder, KVCache, KVPool
 
 pytestmark = pytest.mark.skipif(torch.cuda.is_available(),
                                 reason="passes dummy addresses: a regressed check must not be able to launch")
@@ -100,3 +101,47 @@ def test_sampling_forward_refusals(lib):
                                rope_theta=1e4, kv_block=64, kv_split=512, max_pos=256)
     plain = _lib.bi_forward_workspace_size(cfg, 64, 4, 128, 32)
     assert _lib.bi_forward_sample_workspace_size(cfg, 64, 4, 128, 32) >= plain + 32 * 512 * 4
+
+
+def test_planning_sizes(lib):
+    """Sizes whose index arithmetic would leave 32 bits."""
+    assert lib.bi_block_table_resize(64, 0, (1 << 30) + 1, 64, 1, 1 << 40, 64, 10, 64, 1 << 40, 64, None) == INVALID
+    assert lib.bi_slot_map(16, 16, (1 << 30) + 1, 16, 8, 10, 100, 16, 16, 16, 16, None) == INVALID
+
+
+def test_pool_and_decoder_arguments():
+    """The decoder's own checks, before anything reaches the device."""
+    for sizes in ((0, 4, 4), (4, 0, 4), (4, 4, 0)):
+        with pytest.raises(ValueError, match="positive"):
+            KVPool(*sizes, device="cpu")
+    pool = KVPool(3, 4, 12, device="cpu")
+    for lens in (torch.zeros(2, dtype=torch.int32), torch.zeros(4, dtype=torch.int32), torch.zeros(3),
+                 torch.zeros(6, dtype=torch.int32)[::2]):
+        with pytest.raises(ValueError, match="lens"):
+            pool.resize(lens)
+    dec = object.__new__(Decoder)
+    dec.device = "cpu"
+    cache = KVCache(None, None, 12)
+    prompts = [[1, 2], [3], [4, 5, 6]]
+    rules, u = bi.bi_sampling(), torch.zeros(5, 3)
+    with pytest.raises(ValueError, match="together"):
+        dec.rollout(prompts, 5, cache, None, sampling=rules)
+    for bad in (torch.zeros(3, 5), torch.zeros(5, 3, dtype=torch.float64), torch.zeros(3, 5).T):
+        with pytest.raises(ValueError, match="uniforms"):
+            dec.rollout(prompts, 5, cache, None, sampling=rules, uniforms=bad)
+    for bad in (KVPool(2, 4, 12, device="cpu"), KVPool(3, 4, 13, device="cpu")):  # sequences, blocks beyond the cache
+        with pytest.raises(ValueError, match="pool"):
+            dec.rollout(prompts, 5, cache, None, sampling=rules, uniforms=u, pool=bad)
+    with pytest.raises(ValueError, match="without sampling"):
+        dec.prefill(prompts, cache, None, u=torch.zeros(6))
+    with pytest.raises(ValueError, match="either"):
+        dec.prefill(prompts, cache, None, sampling=rules)
+    with pytest.raises(ValueError, match="either"):
+        dec.prefill(prompts, cache, None, sampling=rules, u=torch.zeros(6), targets=prompts)
+    for bad in (torch.zeros(5), torch.zeros(6, dtype=torch.float64), torch.zeros(12)[::2]):
+        with pytest.raises(ValueError, match="u must"):
+            dec.prefill(prompts, cache, None, sampling=rules, u=bad)
+    few = bi.bi_sampling()
+    few.tensors, few.n = (torch.ones(2), None, None, None), 2
+    with pytest.raises(ValueError, match="fewer"):
+        dec.recompute(prompts, [[1], [2], [3]], cache, None, sampling=few)
