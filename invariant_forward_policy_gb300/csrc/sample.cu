@@ -266,7 +266,7 @@ struct SmpMass {
     const uint2 t = tab[(bits & 63) * kSmpTabLanes];
     const uint32_t M = t.x + (uint32_t)__float_as_int(__fmaf_rn(__uint_as_float(t.y), g, kSmpMagic));
     u64 w;
-    asm("shr.b64 %0, %1, %2;" : "=l"(w) : "l"((u64)M << 32), "r"((shift0 - bits) >> 6));
+    asm("shr.b64 %0, %1, %2;" : "=l"(w) : "l"((u64)M << 32), "r"(((uint32_t)shift0 - (uint32_t)bits) >> 6));
     return w;
   }
 };

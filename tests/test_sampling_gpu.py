@@ -321,3 +321,45 @@ def test_a_captured_step_walks_its_random_numbers():
         st.synchronize()
     assert ids.cpu().tolist() == [-1] * T
     assert bi.bi_device_status() == bi.BI_ERR_DEVICE_CHECK
+
+
+@pytest.mark.parametrize("T,V,ld,dtype", [(3, 129280, 129280, torch.float32), (3, 262144, 262147, torch.bfloat16),
+                                          (160, 129280, 129281, torch.bfloat16), (310, 70001, 70001, torch.float32)])
+@pytest.mark.parametrize("dist", ["flat", "peaked"])
+def test_long_rows_match_the_oracle(T, V, ld, dtype, dist):
+    """Every split of a row, long rows, and the rules side by side in one call; the oracle on a few of the rows."""
+    rng = np.random.default_rng([T, V, len(dist)])
+    x = np.tile(_logits(rng, 8, V, dist), (-(-T // 8), 1))[:T]
+    u = rng.random(T).astype(np.float32)
+    rule = dict(temp=rng.uniform(0.6, 1.2, T), k=rng.choice([0, 1, 50, 300, 700, 1024, 1025, 20000, V, V + 1], T),
+                p=rng.choice([-1.0, 0.0, 0.5, 0.9, 0.999, 1.0, 2.0], T), mp=rng.choice([-1.0, 0.0, 1e-4, 0.05, 1.0], T))
+    ids, lp, stored = _run(x, u, dtype, ld, **rule)
+    for t in rng.choice(T, min(T, 24), replace=False):
+        one = slice(t, t + 1)
+        _check(stored[one], u[one], ids[one], lp[one], **{k: v[t] for k, v in rule.items()})
+    assert bi.bi_device_status() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    """Nothing is shared between calls: two streams, each its own rows, interleaved."""
+    rng = np.random.default_rng(12)
+    T, V = 40, 33000
+    rule = dict(temp=0.8, k=rng.choice([0, 50, 2000], T), p=rng.choice([0.9, 1.0], T))
+    sp = _rule(T, **rule)
+    sides = []
+    for _ in range(2):
+        x = torch.from_numpy(_logits(rng, T, V, "peaked")).cuda()
+        u = torch.from_numpy(rng.random(T).astype(np.float32)).cuda()
+        ids = torch.empty((8, T), dtype=torch.int32, device="cuda")
+        sides.append((x, u, ids, torch.empty((8, T), device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for k in range(8):
+        for x, u, ids, lp, st in sides:
+            bi.bi_sample(x, T, V, sp, u, ids[k], lp[k], stream=st)
+    torch.cuda.synchronize()
+    for x, u, ids, lp, _ in sides:
+        want, wlp = torch.empty_like(ids[0]), torch.empty_like(lp[0])
+        bi.bi_sample(x, T, V, sp, u, want, wlp)
+        for k in range(8):
+            assert torch.equal(ids[k], want) and same_bits(lp[k], wlp)
+    assert bi.bi_device_status() == 0
