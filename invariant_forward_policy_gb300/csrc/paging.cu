@@ -104,6 +104,8 @@ __global__ void __launch_bounds__(kPlanThreads) block_table_resize_kernel(
   }
   long long run = before;
   int mine = 0;
+  bool bad = false;
+  const uint32_t blocks = (uint32_t)n_blocks;
   for (int b0 = first; b0 < last; b0 += kPlanThreads) {
     const int b = b0 + tid;
     Demand d{0, 0, 0, false};
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(kPlanThreads) block_table_resize_kernel(
     run += tile;
     const long long asked = upto & 0xffffffffll, freed = upto >> 32;
     const bool serve = d.more > 0 && asked <= count;
-    if (d.bad || (d.more > 0 && !serve)) report(status, DEV_BAD_INDEX);
+    bad |= d.bad || (d.more > 0 && !serve);
     int4 pl = make_int4(0, 0, 0, 0);
     if (serve) pl = make_int4(owned, d.more, (int)(asked - d.more), 0);
     if (d.less > 0) pl = make_int4(owned - d.less, -d.less, (int)(freed - d.less), 0);
@@ -137,20 +139,22 @@ __global__ void __launch_bounds__(kPlanThreads) block_table_resize_kernel(
         int64_t at = (int64_t)head + e.z + i;
         if (at >= n_blocks) at -= n_blocks;
         const int32_t id = ring[at];
-        if (id < 0 || id >= n_blocks) report(status, DEV_BAD_INDEX);
+        bad |= (uint32_t)id >= blocks;
         row[i] = id;
       }
       for (int i = lane; i < -e.y; i += g) {  // to its tail: never among the free ids, which are being read
         int64_t at = (int64_t)head + count + e.z + i;
         at %= n_blocks;
         const int32_t id = row[i];
-        if ((int64_t)count + e.z + i < n_blocks) ring[at] = id;
-        if ((int64_t)count + e.z + i >= n_blocks || id < 0 || id >= n_blocks) report(status, DEV_BAD_INDEX);
+        const bool fits = (int64_t)count + e.z + i < n_blocks;
+        if (fits) ring[at] = id;
+        bad |= !fits || (uint32_t)id >= blocks;
         row[i] = -1;
       }
     }
     __syncthreads();
   }
+  if (bad) report(status, DEV_BAD_INDEX);
   if (CS == 1) all = run;
   long long handed;
   plan_scan<kPlanThreads>(mine, warp_sums, &handed);
