@@ -444,7 +444,7 @@ size_t bi_lm_head_logprob_workspace_size(int64_t T, int64_t V, int64_t K, int mo
  * whose running kept mass exceeds u times the kept mass S; its logprob is
  * (x_i - max x) / T - ln S.  T = 0 is greedy: the first maximum, logprob 0.
  * bi_sample_logprob gives the same logprob (the same bits) of a given token, or
- * -inf for one that is not kept.  Masses are held to about 3e-10 and summed as
+ * -inf for one that is not kept.  Masses are held to about 5e-10 and summed as
  * integers, so results depend neither on T (the row count) nor on the batch.
  *
  * bi_sampling: device arrays of n entries each, or NULL: temperature (NULL: 1;

@@ -23,17 +23,29 @@
 // (the first from HBM, the others from L2).  The first pass finds the maximum.  Then
 //  - nothing cut but by min-p: one pass sums the masses;
 //  - top_k up to 1024: in each CTA the k'-th largest of the threads' own maxima (known from the read),
-//    k' somewhat above the CTA's share of k, lets through somewhat more than k' logits; one CTA orders
-//    what the CTAs let through and does the rest, provided that the k-th of them is not below any
-//    CTA's bound;
-//  - top-p: a histogram of counts over k = 64 log2 w (1/32 octave) predicts where the cut is; one
+//    k' (384 at most) somewhat above the CTA's share of k, lets through somewhat more than k' logits; one
+//    CTA orders what the CTAs let through and does the rest, provided that the k-th of them is not below
+//    any CTA's bound;
+//  - top-p: a histogram of counts and mean depths (bins of 1/32 octave) predicts where the cut is; one
 //    pass sums the masses and lists the logits next to the prediction, and one CTA orders the list
 //    and finds the cut, exactly;
-//  - anything else (larger top_k, rows of logits beyond 2^13 octaves, a list that overflows, a missed
-//    prediction): one CTA finds the cut from global memory by histograms with masses, on octaves first and
-//    on the float's bits then, until the bin fits the sort or holds equal values only, whose first few
-//    by index are counted out.
+//  - anything else (larger top_k or k', top_k or top-p over logits beyond 2^13 octaves, a list that overflows, a
+//    missed prediction): one CTA finds the cut from global memory by histograms with masses, on octaves
+//    first and on the float's bits then, until the bin fits the sort or holds equal values only, whose
+//    first few by index are counted out.
 // The draw finds the CTA, then the warp, then the token whose running mass crosses u S.
+//
+// What bounds it.  Large batches: instruction issue, not memory.  Reading the logits once would take 39 us for
+// 512 fp32 rows of 129280 and 78 us for 2048 bf16 rows of them or 4096 fp32 rows of 32000.  At temperature
+// alone the calls take 96, 239 and 164 us (a maximum, then about 14 instructions a mass, and the draw), with top_k
+// 182 us for the bf16 rows (the second pass only compares), with top-p 496 and 403 us for the last two: two shared
+// atomics a logit, two sums and a comparison more in the pass of masses, and a dozen barriers a row with one warp's
+// or one CTA's work between them.  Small calls: that chain alone, 11.8 us for one row of 4096 with top-k (launch
+// and exit are 2.5 of them), 14.5 us for 16 rows of 129280 at temperature alone, 29 us with top-p.  The last way
+// costs a row of 129280 some 180 us.  Measured and dropped: rows resident in shared memory (the passes after the first ran no
+// faster than from L2, and fewer rows were in flight); 256 threads and four CTAs an SM, or three of 512 (spills);
+// loads of the next batch under the work of this one; finer bins with counts alone (longer lists); packed
+// two-element arithmetic (the same issue slots).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -129,7 +141,7 @@ struct SmpShared {
   u64 whigh[kSmpWarps];
   uint32_t wcnt[kSmpWarps];
   // written by the cluster's CTAs, each at its rank: what is needed of all of them is then at hand locally
-  float cta_max[8], cta_min[8], cta_bound[8];
+  float cta_max[8], cta_bound[8];
   Sum cta_sum[8], cta_sum2[8];
   uint32_t cta_n[8];
   float x_lo, x_hi;               // top-p's prediction
@@ -624,7 +636,8 @@ struct SmpSolo {
       __syncthreads();
       each([&](int, float x) {
         if (active(x)) {
-          const int b = level == 0 ? min((ms.k_top - ms.k_of(x)) >> kSmpMassShift, kSmpMassBins - 1) : (int)((hi - smp_key(x)) >> shift);
+          const int b = level == 0 ? min((ms.k_top - ms.k_of(x)) >> kSmpMassShift, kSmpMassBins - 1)
+                                   : (int)((hi - smp_key(x)) >> shift);
           const u64 w = ms.mass(x, tab);
           atomicAdd(&h[b], 1u);
           // twelve-bit limbs: 2^18 of them sum to less than 2^30
@@ -776,17 +789,29 @@ struct SmpRow {
     if (CS == 1) return ptr;
     return cl.map_shared_rank(ptr, r);
   }
-  // Appends (warp-converged) to this CTA's segment of rank 0's list; entries beyond it are counted only.
-  BI_DEV void append(bool take, float x, int pos, u64* segment, u64* own) {
-    const unsigned who = __ballot_sync(0xffffffffu, take);
-    if (who == 0u) return;
+  // Appends (warp-converged) those of a lane's four logits, from position p0 on, that take() wants to this CTA's
+  // segment of rank 0's list; entries beyond it are counted only.  (One counter update for all four; with one for each of
+  // them 2048 bf16 rows of 129280 under all rules took 350 us instead of 331.)
+  template <typename F>
+  BI_DEV void append4(F take, const float (&x)[4], int p0, u64* segment, u64* own) {
+    unsigned who[4], n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      who[i] = __ballot_sync(0xffffffffu, take(x[i]));
+      n += __popc(who[i]);
+    }
     uint32_t o = 0;
-    if (lane == 0) o = atomicAdd(&sh.list_n, (uint32_t)__popc(who));
-    o = __shfl_sync(0xffffffffu, o, 0) + __popc(who & ((1u << lane) - 1u));
-    if (take && o < (uint32_t)kSegment) {
-      const u64 e = smp_entry(x, mine.base + pos);
-      segment[o] = e;
-      if (own) own[o] = e;
+    if (lane == 0) o = atomicAdd(&sh.list_n, n);
+    o = __shfl_sync(0xffffffffu, o, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t at_ = o + __popc(who[i] & ((1u << lane) - 1u));
+      if ((who[i] >> lane & 1u) && at_ < (uint32_t)kSegment) {
+        const u64 e = smp_entry(x[i], mine.base + p0 + i);
+        segment[at_] = e;
+        if (own) own[at_] = e;
+      }
+      o += __popc(who[i]);
     }
   }
   // Rank 0: the segments' entries joined at the front of the list (no barrier after it); their number, or -1 when
@@ -981,10 +1006,7 @@ struct SmpRow {
     u64* segment = at(list(), 0) + rank * kSegment;
     mine.template each4<kWide>([&](int p0, const float (&x)[4]) {
       const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-      if (__any_sync(0xffffffffu, top >= bound)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) append(x[i] >= bound, x[i], p0 + i, segment, nullptr);
-      }
+      if (__any_sync(0xffffffffu, top >= bound)) append4([&](float v) { return v >= bound; }, x, p0, segment, nullptr);
     });
     __syncthreads();
     if (tid == 0) {
@@ -1109,9 +1131,11 @@ struct SmpRow {
     const float bottom = fminf(fmaxf(__fmaf_rn(x_min, c11, zero) - 8388608.f, 0.f) + 2.f, 4096.f * (kSmpBins - 1));
     const uint32_t deepest = (uint32_t)bottom;
     uint32_t* depths = counts() + kSmpBins;
+    uint32_t bits = 0;
     mine.template each4<4>([&](int, const float (&x)[4]) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        if (SmpShare<TL>::VE == 4) bits |= __float_as_uint(x[i]);
         const uint32_t d = (uint32_t)__float_as_int(__fmaf_rn(x[i], c11, zero)) - 0x4B000000u;
         if (d < deepest) {  // the open bin would only serialise
           atomicAdd(&counts()[d >> 12], 1u);
@@ -1119,12 +1143,15 @@ struct SmpRow {
         }
       }
     });
+    // 16-bit logits, as they are or widened, stand in few places: a bin's are not spread over it
+    const bool coarse = !__syncthreads_or(SmpShare<TL>::VE == 4 && (bits & 0x1fffu) != 0u);
     csync();
     if (rank == 0) {
       // a bin's mass to second order from its count and mean depth; the open bin's is left out of the prediction
       constexpr int BPT = kSmpBins / kSmpThreads;
       float w[BPT], sum = 0.f;
       bool dense[BPT];
+      const uint32_t many = coarse ? 1024 : 64;
       static_assert(BPT == 2, "a pair of bins per thread");
       uint32_t c[BPT] = {0, 0}, d[BPT] = {0, 0};
 #pragma unroll
@@ -1143,7 +1170,7 @@ struct SmpRow {
         // in units of the maximum's mass; the variance of many depths across a bin adds 2e-5
         const float r = c[i] ? __fdividef(0.5f * z * z - 1.96e-5f, n) + (1.f + 1.96e-5f) * n - z : 0.f;
         w[i] = r * (i ? scale * 0.97857206f : scale);  // 2^(-1/32)
-        dense[i] = c[i] >= 64;
+        dense[i] = c[i] >= many;
         sum += w[i];
       }
       float run = sum;
@@ -1177,7 +1204,9 @@ struct SmpRow {
         const int b = tid * BPT + i;
         if (b < kSmpBins - 2) {
           // within a bin of many, at the fraction of its mass, give or take what n places at random leave open
-          // (2.2 / sqrt(n) of a bin); else at the bin's end; and a little further
+          // (2.2 / sqrt(n) of a bin); else at the bin's end; and a little further.  (Whole bins of up to 1024 for
+          // coarse logits, whose ties a fraction misses: 2048 bf16 rows of 129280 719 -> 499 us; for others their
+          // longer list costs more than it saves: 4096 fp32 rows of 32000 390 -> 434 us.)
           const float give = 0.1f + (dense[i] ? 4.4f * rsqrtf((float)c[i]) : 0.f);
           if (run < g_hi && g_hi <= next) {
             const float part = dense[i] ? __fdividef(g_hi - run, w[i]) : 0.f;
@@ -1229,10 +1258,8 @@ struct SmpRow {
               if (x[i] > x_hi) some_above += w;
               near = fminf(near, fabsf(x[i] - mid));
             }
-            if (__any_sync(0xffffffffu, near <= half)) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) append(x[i] <= x_hi && x[i] >= x_lo, x[i], p0 + i, segment, own);
-            }
+            if (__any_sync(0xffffffffu, near <= half))
+              append4([&](float v) { return v <= x_hi && v >= x_lo; }, x, p0, segment, own);
           },
           [&] {
             all += some;
@@ -1519,10 +1546,12 @@ static bi_status launch_sample(const SampleArgs& a, int64_t T, cudaStream_t st) 
 template <typename TL>
 static bi_status dispatch_sample_as(SampleArgs& a, int64_t T, cudaStream_t st) {
   // Bits do not depend on the split.  A row is split while the rows alone leave CTA slots (two per SM) idle, down to
-  // 2K logits a CTA.
+  // 2K logits a CTA: 64 rows of 129280 with top-k and top-p took 33, 27, 22 and 31 us on 1, 2, 4 and 8 CTAs a row (4 is
+  // the rule's), and 4096 rows of 32000 at temperature alone 185 us on one and 303 us on two (1 is).
   int cs = 1;
   while (cs < 8 && cdiv(a.V, cs) > 2048 && T * cs * 2 <= 2 * num_sms()) cs *= 2;
-  // The rows in flight have to stay in L2 until their last pass: a row of more than 256 KB is split too.
+  // The rows in flight have to stay in L2 until their last pass: a row of more than 256 KB is split too (512 fp32 rows
+  // of 129280 at temperature alone: 112 us unsplit, 100 us on two CTAs).
   if (cs == 1 && a.V * (int64_t)sizeof(TL) > 256 * 1024) cs = a.V * (int64_t)sizeof(TL) > 512 * 1024 ? 4 : 2;
   a.share = (int)(cdiv(cdiv(a.V, cs), 8) * 8);
   switch (cs) {
@@ -1541,7 +1570,8 @@ static bi_status sample_args(const char* who, const void* logits, int dtype, int
                              const bi_sampling* sp, const int32_t* param_row, SampleArgs* a) {
   auto bad = [&](bi_status st, const char* what) { return fail(st, std::string(who) + ": " + what); };
   if (!logits) return bad(BI_ERR_INVALID_ARG, "null logits");
-  if (dtype != BI_DTYPE_FP32 && dtype != BI_DTYPE_BF16) return bad(BI_ERR_INVALID_ARG, "dtype must be BI_DTYPE_FP32 or BI_DTYPE_BF16");
+  if (dtype != BI_DTYPE_FP32 && dtype != BI_DTYPE_BF16)
+    return bad(BI_ERR_INVALID_ARG, "dtype must be BI_DTYPE_FP32 or BI_DTYPE_BF16");
   if (V < 1 || ld < V) return bad(BI_ERR_INVALID_ARG, "V must be positive and ld at least V");
   static_assert(kSmpMaxV == kMaxSampleVocab, "vocabulary limit");
   if (V > kSmpMaxV) return bad(BI_ERR_UNSUPPORTED_SHAPE, "V must be at most 262144");
@@ -1556,7 +1586,8 @@ static bi_status sample_args(const char* who, const void* logits, int dtype, int
   if (sp) {
     const bool any = sp->temperature || sp->top_k || sp->top_p || sp->min_p;
     if (any && sp->n < 1) return bad(BI_ERR_INVALID_ARG, "sampling parameters need n >= 1");
-    if (any && !param_row && sp->n < T) return bad(BI_ERR_INVALID_ARG, "fewer sampling parameters than rows and no param_row");
+    if (any && !param_row && sp->n < T)
+      return bad(BI_ERR_INVALID_ARG, "fewer sampling parameters than rows and no param_row");
     a->temperature = sp->temperature;
     a->top_k = sp->top_k;
     a->top_p = sp->top_p;
