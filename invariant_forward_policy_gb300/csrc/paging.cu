@@ -325,8 +325,9 @@ bi_status bi_slot_map(const int32_t* new_tokens, const int32_t* start, int64_t B
   BI_REQUIRE(B <= 1 << 30 && n_blocks <= 0x7fffffff, "too many requests or blocks");
   BI_REQUIRE(T <= 0x7fffffff, "T too large");
   const dim3 grid((unsigned)std::max<int64_t>(1, cdiv(T, kMapRows)));
-  return launched(launch_pdl(slot_map_kernel, grid, dim3(kMapThreads), 0, as_stream(stream), new_tokens, start, (int)B, block_table, max_blocks_per_seq, n_blocks, T,
-                             row0, row_seq, row_pos, slots, device_status_ptr()),
+  return launched(launch_pdl(slot_map_kernel, grid, dim3(kMapThreads), 0, as_stream(stream), new_tokens, start, (int)B,
+                             block_table, max_blocks_per_seq, n_blocks, T, row0, row_seq, row_pos, slots,
+                             device_status_ptr()),
                   "bi_slot_map");
 }
 
