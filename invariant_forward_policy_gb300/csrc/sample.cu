@@ -37,13 +37,13 @@
 //
 // What bounds it.  Large batches: instruction issue, not memory.  Reading the logits once would take 39 us for
 // 512 fp32 rows of 129280 and 78 us for 2048 bf16 rows of them or 4096 fp32 rows of 32000.  At temperature
-// alone the calls take 96, 239 and 164 us (a maximum, then about 14 instructions a mass, and the draw), with top_k
-// 182 us for the bf16 rows (the second pass only compares), with top-p 496 and 403 us for the last two: two shared
-// atomics a logit, two sums and a comparison more in the pass of masses, and a dozen barriers a row with one warp's
-// or one CTA's work between them.  Small calls: that chain alone, 11.8 us for one row of 4096 with top-k (launch
-// and exit are 2.5 of them), 14.5 us for 16 rows of 129280 at temperature alone, 29 us with top-p.  The last way
-// costs a row of 129280 some 180 us.  Measured and dropped: rows resident in shared memory (the passes after the first ran no
-// faster than from L2, and fewer rows were in flight); 256 threads and four CTAs an SM, or three of 512 (spills);
+// alone the calls take 96, 244 and 164 us (23 instructions a logit), with top_k 178 us for the bf16 rows (the second
+// pass only compares), with top-p 486 and 378 us for the last two: 49 instructions a logit (12 of them the counts, two
+// shared atomics among them), 24,000 warp instructions a row beside them, and a dozen barriers.  Small calls: that
+// chain alone, 12.0 us for one row of 4096 with top-k (launch and exit are 2.5 of them), 14.5 us for 16 rows of
+// 129280 at temperature alone, 29 us with top-p.  The last way costs a row of 129280 some 180 us.  Measured and
+// dropped: rows resident in shared memory (the passes after the first ran no faster than from L2, and fewer rows
+// were in flight); 256 threads and four CTAs an SM, or three of 512 (spills);
 // loads of the next batch under the work of this one; finer bins with counts alone (longer lists); packed
 // two-element arithmetic (the same issue slots).
 #include <cooperative_groups.h>
@@ -789,29 +789,15 @@ struct SmpRow {
     if (CS == 1) return ptr;
     return cl.map_shared_rank(ptr, r);
   }
-  // Appends (warp-converged) those of a lane's four logits, from position p0 on, that take() wants to this CTA's
-  // segment of rank 0's list; entries beyond it are counted only.  (One counter update for all four; with one for each of
-  // them 2048 bf16 rows of 129280 under all rules took 350 us instead of 331.)
-  template <typename F>
-  BI_DEV void append4(F take, const float (&x)[4], int p0, u64* segment, u64* own) {
-    unsigned who[4], n = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      who[i] = __ballot_sync(0xffffffffu, take(x[i]));
-      n += __popc(who[i]);
-    }
-    uint32_t o = 0;
-    if (lane == 0) o = atomicAdd(&sh.list_n, n);
-    o = __shfl_sync(0xffffffffu, o, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t at_ = o + __popc(who[i] & ((1u << lane) - 1u));
-      if ((who[i] >> lane & 1u) && at_ < (uint32_t)kSegment) {
-        const u64 e = smp_entry(x[i], mine.base + p0 + i);
-        segment[at_] = e;
-        if (own) own[at_] = e;
-      }
-      o += __popc(who[i]);
+  // Appends to this CTA's segment of rank 0's list, a lane for itself; entries beyond it are counted only.  (Few groups
+  // of 128 logits have more than one: with the warp's lanes voting on all of a group's 4096 fp32 rows of 32000 under
+  // top-p took 403 us instead of 378, 2048 bf16 rows of 129280 under all rules 331 instead of 320.)
+  BI_DEV void append(float x, int p, u64* segment, u64* own) {
+    const uint32_t o = atomicAdd(&sh.list_n, 1u);
+    if (o < (uint32_t)kSegment) {
+      const u64 e = smp_entry(x, mine.base + p);
+      segment[o] = e;
+      if (own) own[o] = e;
     }
   }
   // Rank 0: the segments' entries joined at the front of the list (no barrier after it); their number, or -1 when
@@ -1006,7 +992,11 @@ struct SmpRow {
     u64* segment = at(list(), 0) + rank * kSegment;
     mine.template each4<kWide>([&](int p0, const float (&x)[4]) {
       const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-      if (__any_sync(0xffffffffu, top >= bound)) append4([&](float v) { return v >= bound; }, x, p0, segment, nullptr);
+      if (top >= bound) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (x[i] >= bound) append(x[i], p0 + i, segment, nullptr);
+      }
     });
     __syncthreads();
     if (tid == 0) {
@@ -1258,8 +1248,11 @@ struct SmpRow {
               if (x[i] > x_hi) some_above += w;
               near = fminf(near, fabsf(x[i] - mid));
             }
-            if (__any_sync(0xffffffffu, near <= half))
-              append4([&](float v) { return v <= x_hi && v >= x_lo; }, x, p0, segment, own);
+            if (near <= half) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (x[i] <= x_hi && x[i] >= x_lo) append(x[i], p0 + i, segment, own);
+            }
           },
           [&] {
             all += some;
