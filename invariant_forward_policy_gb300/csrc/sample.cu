@@ -17,7 +17,7 @@
 // exponential, ACM TOMS 15, 1989) times a cubic in the remainder, whose argument is reduced in two
 // floats, about 5e-10 relative.  Integer sums have no order, every quantity below is defined by
 // them alone, and so a row's bits depend neither on how many CTAs share it, nor on which of the
-// ways to its cut below was taken, nor on T.
+// ways to its cut below was taken, nor on the batch.
 //
 // A row is shared by a cluster of 1, 2, 4 or 8 CTAs, each with a contiguous share that its passes stream
 // (the first from HBM, the others from L2).  The first pass finds the maximum.  Then
@@ -43,9 +43,8 @@
 // chain alone, 12.0 us for one row of 4096 with top-k (launch and exit are 2.5 of them), 14.5 us for 16 rows of
 // 129280 at temperature alone, 29 us with top-p.  The last way costs a row of 129280 some 180 us.  Measured and
 // dropped: rows resident in shared memory (the passes after the first ran no faster than from L2, and fewer rows
-// were in flight); 256 threads and four CTAs an SM, or three of 512 (spills);
-// loads of the next batch under the work of this one; finer bins with counts alone (longer lists); packed
-// two-element arithmetic (the same issue slots).
+// were in flight); 256 threads and four CTAs an SM, or three of 512 (spills); loads of the next batch under the work
+// of this one; finer bins with counts alone (longer lists); packed two-element arithmetic (the same issue slots).
 #include <cooperative_groups.h>
 
 #include <algorithm>
