@@ -30,7 +30,7 @@
 //    pass sums the masses and lists the logits next to the prediction, and one CTA orders the list
 //    and finds the cut, exactly;
 //  - anything else (larger top_k or k', top_k or top-p over logits beyond 2^13 octaves, a list that overflows, a
-//    missed prediction): one CTA finds the cut from global memory by histograms with masses, on octaves
+//    missed prediction, u = 0): one CTA finds the cut from global memory by histograms with masses, on octaves
 //    first and on the float's bits then, until the bin fits the sort or holds equal values only, whose
 //    first few by index are counted out.
 // The draw finds the CTA, then the warp, then the token whose running mass crosses u S.
@@ -740,12 +740,19 @@ struct SmpSolo {
     }
     const float cut_x = smp_unkey(cut.key);
     const int32_t id = sh.id;
-    locate([&](int i, float x) { return x > cut_x || (x == cut_x && i <= cut.idx) ? ms.mass(x, tab) : 0ull; },
-           [&](Sum S) { return out.a.ids_in ? S : smp_draw_target(sh.u, S); },
+    const bool first = !out.a.ids_in && sh.u == 0.f;
+    auto kept = [&](int i, float x) { return x > cut_x || (x == cut_x && i <= cut.idx); };
+    locate([&](int i, float x) { return kept(i, x) ? ms.mass(x, tab) : 0ull; },
+           [&](Sum S) { return out.a.ids_in || first ? S : smp_draw_target(sh.u, S); },
            [&](int i, float x, Sum S) {
-             if (!out.a.ids_in) out.token(ms, sh, tab, i, x, S);
-             else sh.total2 = S;
+             if (out.a.ids_in || first) sh.total2 = S;
+             else out.token(ms, sh, tab, i, x, S);
            });
+    if (first) {  // u = 0: the first kept token of any mass, also one below the unit (2^-1074 is what 64 bits hold)
+      const float x_pos = (float)((double)ms.m - 745.13 / (double)sh.r_hi);
+      locate([&](int i, float x) { return kept(i, x) && x >= x_pos ? 1ull : 0ull; }, [](Sum) { return (Sum)1; },
+             [&](int i, float x, Sum) { out.token(ms, sh, tab, i, x, sh.total2); });
+    }
     if (out.a.ids_in && tid == 0) {
       const float x = sh.x_id;
       if (x > cut_x || (x == cut_x && id <= cut.idx)) out.token(ms, sh, tab, id, x, sh.total2);
@@ -1471,7 +1478,8 @@ struct SmpRow {
       t_min = fminf(t_min, __shfl_xor_sync(0xffffffffu, t_min, o));
     }
     const int k_eff = sh.k_eff;
-    if (k_eff < a.V && k_eff <= kSmpMaxK) {
+    const bool first = !score && sh.u == 0.f && k_eff > 1;  // masses do not tell: the rare way
+    if (!first && k_eff < a.V && k_eff <= kSmpMaxK) {
       // a CTA's share of k, with four of its standard deviations
       const float part = (float)k_eff / CS;
       const int k = CS == 1 ? k_eff : min(k_eff, (int)(part + 4.f * sqrtf(part)) + 8);
@@ -1483,7 +1491,9 @@ struct SmpRow {
     if (tid < CS) at(sh.cta_max, tid)[rank] = mx;
     csync();
     if (!row_max()) return;
-    if (k_eff == a.V && sh.p >= 1.f) {
+    if (first) {
+      if (rank == 0) solo();
+    } else if (k_eff == a.V && sh.p >= 1.f) {
       if (absolute()) plain<true>();
       else plain<false>();
     } else if (k_eff == a.V && absolute()) {

@@ -363,3 +363,23 @@ def test_calls_on_two_streams_at_once():
         for k in range(8):
             assert torch.equal(ids[k], want) and same_bits(lp[k], wlp)
     assert bi.bi_device_status() == 0
+
+
+@pytest.mark.parametrize("rule", ["temp", "topk", "topk_large", "topp", "minp", "topk_topp"])
+@pytest.mark.parametrize("V", [1, 2, 35, 2031, 40001])
+def test_zero_draws_the_first_token_of_any_mass(rule, V):
+    """u = 0: masses far below the fixed-point unit count, those that 64 bits do not hold do not; the next u after
+    it, on rows with nothing so small, is the first token too."""
+    rng = np.random.default_rng([V, len(rule)])
+    T = 6
+    x = (300.0 * rng.standard_normal((T, V))).astype(np.float32)
+    x[:, 0] = x.max(1) - np.float32([0.0, 30.0, 60.0, 200.0, 3000.0, np.inf])   # of the largest's mass, or of none
+    r = dict(RULES[rule])
+    u = np.zeros(T, np.float32)
+    ids, lp, st = _run(x, u, **r)
+    _check(st, u, ids, lp, **r)
+    x = rng.standard_normal((T, V)).astype(np.float32)
+    u[:] = 2.0 ** -40
+    ids, lp, st = _run(x, u, **r)
+    _check(st, u, ids, lp, **r)
+    assert bi.bi_device_status() == 0
