@@ -64,7 +64,7 @@ def _run(x, u, dtype=torch.float32, ld=None, **rule):
 def _tol(z, lp):
     """The logprob is (x - m)/T - e ln2 - ln(mant): the two-float product's high part enters a fused multiply-add
     and two sums, each rounded at 2^-24 of a term no larger than |z| + |lp| + 1; logf's error is within 2^-23 of
-    at most 0.41.  The masses (3e-10 each, cut at 2^-45 of the largest: 2^18 of them at most) add 1e-8."""
+    at most 0.41.  The masses (5e-10 each, cut at 2^-56 of the largest: 2^18 of them at most) add 1e-8."""
     return 2.0 ** -24 * (3 * (np.abs(z) + np.abs(lp) + 1) + 1) + 1e-8
 
 
