@@ -297,6 +297,7 @@ BI_DEV float smp_logprob(float x, float m, float r_hi, float r_lo, Sum S, Sum W)
   float dl;
   const float d = smp_diff(x, m, &dl);
   const float ah = __fmul_rn(d, r_hi);
+  if (ah == -INFINITY) return ah;  // d or d / T beyond fp32 (a logit of the lowest value at T < 1), as is the logprob
   const float al = __fadd_rn(__fmaf_rn(d, r_hi, -ah), __fmaf_rn(d, r_lo, __fmul_rn(dl, r_hi)));
   float sh, sl, wh, wl;
   int es, ew;
