@@ -295,9 +295,14 @@ BI_DEV void smp_split(Sum v, float& h, float& l, int& e) {
 // floats until the last sum.
 BI_DEV float smp_logprob(float x, float m, float r_hi, float r_lo, Sum S, Sum W) {
   float dl;
-  const float d = smp_diff(x, m, &dl);
+  float d = smp_diff(x, m, &dl);
+  if (d == -INFINITY) {  // x - m beyond fp32, which (x - m) / T need not be: of the halves
+    d = smp_diff(0.5f * x, 0.5f * m, &dl);
+    r_hi *= 2.f;
+    r_lo *= 2.f;
+  }
   const float ah = __fmul_rn(d, r_hi);
-  if (ah == -INFINITY) return ah;  // d or d / T beyond fp32 (a logit of the lowest value at T < 1), as is the logprob
+  if (ah == -INFINITY) return ah;  // a logit of the lowest value at T < 1: the logprob is beyond fp32
   const float al = __fadd_rn(__fmaf_rn(d, r_hi, -ah), __fmaf_rn(d, r_lo, __fmul_rn(dl, r_hi)));
   float sh, sl, wh, wl;
   int es, ew;
