@@ -1406,7 +1406,9 @@ struct SmpRow {
       else ok = false;
     } else {
       const int64_t ur = a.u_row ? (int64_t)*a.u_row : 0;
-      if (ur >= 0 && ur < a.u_rows) u = a.u[ur * a.u_ld + (a.dst ? (int64_t)a.dst[row] : row)];
+      // (-0 -> +0: the products with u take it apart without a sign)
+      if (ur >= 0 && ur < a.u_rows)
+        u = __fadd_rn(a.u[ur * a.u_ld + (a.dst ? (int64_t)a.dst[row] : row)], 0.f);
       else ok = false;
       ok = ok && u >= 0.f && u < 1.f;
     }
