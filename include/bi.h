@@ -442,12 +442,14 @@ size_t bi_lm_head_logprob_workspace_size(int64_t T, int64_t V, int64_t K, int mo
  *   top_p: the shortest prefix of what is left with at least top_p of its mass.
  * bi_sample draws, for a given u in [0, 1), the first token in index order
  * whose running kept mass exceeds u times the kept mass S; its logprob is
- * (x_i - max x) / T - ln S.  A mass below 2^-1074 is 0.  T = 0 is greedy: the
- * first maximum, logprob 0.  bi_sample_logprob gives the same logprob (the same
- * bits) of a given token, or -inf for one that is not kept.  Masses are held to
- * about 5e-10, in units of 2^-56 (u = 0 draws the first token of any mass all
- * the same), and summed as integers, so results depend neither on T (the row
- * count) nor on the batch.
+ * (x_i - max x) / T - ln S.  A mass that 64 bits round to 0 (2^-1075 and
+ * less) is 0: its token is kept or cut by its place in the order like any
+ * other and has that logprob when it is kept, but no u draws it.  T = 0 is
+ * greedy: the first maximum, logprob 0.  A logprob beyond fp32 is -inf.
+ * bi_sample_logprob gives the same logprob (the same bits) of a given token, or
+ * -inf for one that is not kept.  Masses are held to about 5e-10, in units of
+ * 2^-56 (u = 0 draws the first token of any mass all the same), and summed as
+ * integers, so results depend neither on T (the row count) nor on the batch.
  *
  * bi_sampling: device arrays of n entries each, or NULL: temperature (NULL: 1;
  * 0, or 2^-64 to 2^64), top_k (NULL, <= 0 or >= V: off), top_p (NULL or >= 1:

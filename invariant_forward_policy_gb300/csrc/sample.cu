@@ -754,8 +754,10 @@ struct SmpSolo {
              if (out.a.ids_in || first) sh.total2 = S;
              else out.token(ms, sh, tab, i, x, S);
            });
-    if (first) {  // u = 0: the first kept token of any mass, also one below the unit (2^-1074 is what 64 bits hold)
-      const float x_pos = (float)((double)ms.m - 745.13 / (double)sh.r_hi);
+    if (first) {
+      // u = 0: the first kept token of any mass, also one below the unit: 64 bits hold masses above 2^-1075, which
+      // round to 2^-1074 and more
+      const float x_pos = __double2float_ru((double)ms.m - 745.13321910194122 / ((double)sh.r_hi + (double)sh.r_lo));
       locate([&](int i, float x) { return kept(i, x) && x >= x_pos ? 1ull : 0ull; }, [](Sum) { return (Sum)1; },
              [&](int i, float x, Sum) { out.token(ms, sh, tab, i, x, sh.total2); });
     }

@@ -3,7 +3,8 @@
 [Article] §2 asks that discrete choices and logprobs be the row's own.  The definition is the
 library's: masses w_i = exp((x_i - max x) / T), tokens ordered by (logit descending, index
 ascending), a kept prefix cut by min-p, then top-k, then top-p, and the draw in index order.
-Nothing here is blocked, binned or fixed-point.
+Nothing here is blocked, binned or fixed-point.  A token whose mass rounds to 0 in 64 bits is kept or cut by
+its place in the order like any other, has the formula's logprob when kept, and is drawn by no u.
 
 [Article] is "vLLM Achieves Bitwise-Consistent RL Training: Eliminating Numerical
 Drift to Zero KL Divergence on DeepSeek-V4-Flash at 91% Throughput"; section numbers
