@@ -176,8 +176,11 @@ bi_status bi_rope_table(float* rope_table, int64_t max_pos, int hd, double theta
  * (counting those that failed), or that needs more than max_blocks_per_seq
  * blocks, keeps what it has and sets the device status; n_owned_out tells
  * which.  A block id outside [0, n_blocks), in the ring or in a surplus entry,
- * is moved as it is and sets the device status.  n_owned_out [B] and pool_out [2] receive the new counts: the inputs
- * themselves, or other arrays (the table and the ring change either way).
+ * is moved as it is and sets the device status.  Blocks given back beyond the
+ * ring's n_blocks places (requests held more than the pool has) are dropped, not
+ * counted, and set the device status.  n_owned_out [B] and pool_out [2] receive
+ * the new counts: the inputs themselves, or other arrays (the table and the ring
+ * change either way).
  * lens, n_owned: device int32 [B].  extra in [0, 2^31) is added to every
  * positive length (a decode step passes its positions and extra = 1).
  *

@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(kPlanThreads) block_table_resize_kernel(
   if (rank == 0 && tid == 0) {
     const int64_t h = (int64_t)head + handed;
     pool_out[0] = (int)(h >= n_blocks ? h - n_blocks : h);
-    pool_out[1] = (int)min((long long)n_blocks, count - handed + (all >> 32));
+    // what was given back beyond the ring's places is not in it
+    pool_out[1] = (int)(count - handed + min((long long)n_blocks - count, all >> 32));
   }
 }
 
