@@ -180,7 +180,8 @@ bi_status bi_rope_table(float* rope_table, int64_t max_pos, int hd, double theta
  * ring's n_blocks places (requests held more than the pool has) are dropped, not
  * counted, and set the device status.  n_owned_out [B] and pool_out [2] receive
  * the new counts: the inputs themselves, or other arrays (the table and the ring
- * change either way).
+ * change either way).  A head outside [0, n_blocks) or a count outside
+ * [0, n_blocks] changes nothing, gives the old counts and sets the device status.
  * lens, n_owned: device int32 [B].  extra in [0, 2^31) is added to every
  * positive length (a decode step passes its positions and extra = 1).
  *

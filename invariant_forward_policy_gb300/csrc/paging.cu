@@ -85,7 +85,12 @@ __global__ void __launch_bounds__(kPlanThreads) block_table_resize_kernel(
   const int head = pool[0], count = pool[1];
   if (tid == 0) served = 0;
   if (head < 0 || head >= n_blocks || count < 0 || count > n_blocks) {  // not a ring: nothing is changed
-    if (rank == 0 && tid == 0) report(status, DEV_BAD_INDEX);
+    for (int b = first + tid; b < last; b += kPlanThreads) n_owned_out[b] = n_owned[b];
+    if (rank == 0 && tid == 0) {
+      pool_out[0] = head;
+      pool_out[1] = count;
+      report(status, DEV_BAD_INDEX);
+    }
     return;
   }
   long long before = 0, all = 0;

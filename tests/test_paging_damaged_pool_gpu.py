@@ -37,3 +37,19 @@ def test_blocks_that_do_not_fit_the_ring_are_not_counted(B, free):
     bi.bi_block_table_resize(_i32(lens), B, d_table, 4, d_owned, ring, 4, pool)
     assert bi.bi_device_status() == 0
     assert d_table[0].cpu().tolist() == [1, 2, 3, -1] and pool.cpu().tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("B", [2, 300])
+@pytest.mark.parametrize("bad", [[-1, 3], [10, 3], [0, 11], [0, -1]])
+def test_a_bad_pool_leaves_its_counts_in_other_arrays_too(B, bad):
+    """Nothing is changed, so the new counts are the old ones."""
+    owned = np.arange(B) % 3
+    table = np.full((B, 4), -1)
+    d_table, d_owned, ring, pool = _i32(table), _i32(owned), _i32(np.arange(10)), _i32(bad)
+    owned_out, pool_out = _i32(np.full(B, -7)), _i32([-7, -7])
+    bi.bi_block_table_resize(_i32(np.full(B, 64)), B, d_table, 4, d_owned, ring, 10, pool, n_owned_out=owned_out,
+                             pool_out=pool_out)
+    assert bi.bi_device_status() == bi.BI_ERR_DEVICE_CHECK
+    assert owned_out.cpu().tolist() == owned.tolist() == d_owned.cpu().tolist()
+    assert pool_out.cpu().tolist() == bad == pool.cpu().tolist()
+    assert (d_table == -1).all() and ring.cpu().tolist() == list(range(10))
