@@ -109,6 +109,24 @@ class KVPool:
         self.ring = torch.from_numpy(block_ids(1, n_blocks, seed)[0]).to(device)
         self.pool = torch.tensor([0, n_blocks], dtype=torch.int32, device=device)
 
+    def check(self, first, last):
+        """Raises ValueError unless the pool can bring every sequence b to first[b] tokens in one resize and
+        from there, a call at a time, to last[b] (host numbers; the counts are read back from the device)."""
+        owned = self.owned.cpu().numpy().astype(np.int64)
+        head, count = self.pool.tolist()
+        held = int(owned.sum())
+        if (not 0 <= head < self.n_blocks or not 0 <= count or count + held > self.n_blocks
+                or owned.min() < 0 or owned.max() > self.max_blocks):
+            raise ValueError(f"not a pool: head {head}, {count} free and {held} held of {self.n_blocks} blocks")
+        now, end = (-(-np.asarray(n, np.int64) // 64) for n in (first, last))
+        if end.max() > self.max_blocks:
+            raise ValueError(f"a sequence needs {end.max()} blocks of at most {self.max_blocks}")
+        # what a call gives back serves later calls only
+        grown = int(np.maximum(now - owned, 0).sum())
+        if grown > count or int(end.sum()) > count + held:
+            raise ValueError(f"the sequences need {grown} more blocks at once and {int(end.sum())} in the end; "
+                             f"the pool has {count} free and {held} held by them")
+
     def resize(self, lens: torch.Tensor, extra: int = 0):
         """Blocks for lens + extra tokens of every sequence (int32 [n_seq] on the device; 0: all given back)."""
         if lens.dtype != torch.int32 or tuple(lens.shape) != (self.n_seq,) or not lens.is_contiguous():
@@ -271,7 +289,8 @@ class Decoder:
         Greedy, or with `sampling` (bi_sampling, one entry per sequence) drawn with
         `uniforms` (fp32 [n_gen, B] on the device, in [0, 1)): token j of sequence b
         with uniforms[j, b].  With `pool` the block table is the pool's (`block_table`
-        is not used) and every step takes the blocks it grows into."""
+        is not used) and every step takes the blocks it grows into; a pool that
+        cannot hold the whole rollout is refused (ValueError) before it starts."""
         B = len(prompts)
         if (sampling is None) != (uniforms is None):
             raise ValueError("sampling and uniforms go together")
@@ -282,6 +301,11 @@ class Decoder:
             raise ValueError(f"the pool must be one of {B} sequences and at most {cache.n_blocks} blocks")
         lens = np.array([len(p) for p in prompts])
         max_ctx = int(lens.max()) + n_gen
+        if pool is not None:
+            if n_gen > 1 and -(-max_ctx // 64) > pool.max_blocks:
+                raise ValueError(f"decode steps of up to {max_ctx} positions need {-(-max_ctx // 64)} blocks of at "
+                                 f"most {pool.max_blocks} a sequence")
+            pool.check(lens, lens + n_gen - 1)
         dev = self.device
         last = torch.from_numpy(np.cumsum(lens) - 1).to(dev)
         pos = torch.from_numpy(lens.astype(np.int32)).to(dev)
