@@ -127,6 +127,14 @@ class KVPool:
             raise ValueError(f"the sequences need {grown} more blocks at once and {int(end.sum())} in the end; "
                              f"the pool has {count} free and {held} held by them")
 
+    def saved(self):
+        """Copies of the device state, for restore()."""
+        return [t.clone() for t in (self.table, self.owned, self.ring, self.pool)]
+
+    def restore(self, saved):
+        for t, s in zip((self.table, self.owned, self.ring, self.pool), saved):
+            t.copy_(s)
+
     def resize(self, lens: torch.Tensor, extra: int = 0):
         """Blocks for lens + extra tokens of every sequence (int32 [n_seq] on the device; 0: all given back)."""
         if lens.dtype != torch.int32 or tuple(lens.shape) != (self.n_seq,) or not lens.is_contiguous():
@@ -290,7 +298,8 @@ class Decoder:
         `uniforms` (fp32 [n_gen, B] on the device, in [0, 1)): token j of sequence b
         with uniforms[j, b].  With `pool` the block table is the pool's (`block_table`
         is not used) and every step takes the blocks it grows into; a pool that
-        cannot hold the whole rollout is refused (ValueError) before it starts."""
+        cannot hold the whole rollout is refused (ValueError) before it starts, and a
+        call that raises leaves the pool's tables and counts as they were."""
         B = len(prompts)
         if (sampling is None) != (uniforms is None):
             raise ValueError("sampling and uniforms go together")
@@ -306,6 +315,20 @@ class Decoder:
                 raise ValueError(f"decode steps of up to {max_ctx} positions need {-(-max_ctx // 64)} blocks of at "
                                  f"most {pool.max_blocks} a sequence")
             pool.check(lens, lens + n_gen - 1)
+        args = (prompts, lens, n_gen, max_ctx, cache, block_table, chunk, use_graph, mode, prefill_max_tokens, sampling,
+                uniforms, pool)
+        if pool is None:
+            return self._rollout(*args)
+        saved = pool.saved()
+        try:
+            return self._rollout(*args)
+        except Exception:
+            pool.restore(saved)
+            raise
+
+    def _rollout(self, prompts, lens, n_gen, max_ctx, cache, block_table, chunk, use_graph, mode, prefill_max_tokens,
+                 sampling, uniforms, pool):
+        B = len(prompts)
         dev = self.device
         last = torch.from_numpy(np.cumsum(lens) - 1).to(dev)
         pos = torch.from_numpy(lens.astype(np.int32)).to(dev)

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+import invariant_forward_policy_gb300 as bi
 from invariant_forward_policy_gb300.decoder import Decoder, KVCache, KVPool
 from oracle import paging
 
@@ -80,3 +81,49 @@ def test_what_the_check_lets_through_is_served():
         assert refused == failed, (owned, nb, lens, n_gen)
         outcomes[failed] += 1
     assert min(outcomes) > 20                                 # both happen
+
+
+def test_taken_blocks_are_put_back():
+    """What `saved` and `restore` of a pool hold, on the host."""
+    pool = _pool(2, 4, 9, owned=[1, 2], head=4)
+    before = [t.clone() for t in (pool.table, pool.owned, pool.ring, pool.pool)]
+    held = pool.saved()
+    for t in (pool.table, pool.owned, pool.ring, pool.pool):
+        t.fill_(-5)
+    pool.restore(held)
+    assert all(torch.equal(a, b) for a, b in zip(before, (pool.table, pool.owned, pool.ring, pool.pool)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sampled", [False, True])
+def test_a_refused_call_gives_its_blocks_back(sampled):
+    """Arguments that the forward calls refuse: the pool is as it was, and serves the corrected call."""
+    from synthetic import DecoderShape, make_decoder_weights, make_prompts
+    from tests.gpu_util import same_bits
+    shape = DecoderShape(2, 128, 4, 2, 64, 256, 2048)
+    dec = Decoder(shape, make_decoder_weights(shape, seed=81, w_std=0.05), max_pos=256)
+    B, mb, n_gen = 3, 4, 9
+    prompts = make_prompts(B, 30, 120, shape.vocab, seed=82)
+    u = torch.rand((n_gen, B), generator=torch.Generator(device="cuda").manual_seed(83), device="cuda")
+    kw = dict(sampling=bi.bi_sampling(), uniforms=u) if sampled else {}
+    pool = KVPool(B, mb, B * mb, seed=5)
+    pool.resize(torch.tensor([70, 0, 10], dtype=torch.int32, device="cuda"))
+    before = [t.clone() for t in (pool.table, pool.owned, pool.ring, pool.pool)]
+    cache = dec.alloc_cache(B * mb)
+    bad = [dict(chunk=0), dict(prefill_max_tokens=0), dict(mode=7)]
+    if sampled:
+        bad.append(dict(sampling=bi.bi_sampling(torch.ones(B - 1, device="cuda"))))
+        bad.append(dict(uniforms=u.cpu()))
+    for b in bad:
+        with pytest.raises(Exception):
+            dec.rollout(prompts, n_gen, cache, None, pool=pool, **{**kw, **b})
+        assert all(torch.equal(a, c) for a, c in zip(before, (pool.table, pool.owned, pool.ring, pool.pool))), b
+    wide = KVPool(1, 8, 8)                                    # past max_pos in the model, not in the table
+    with pytest.raises(Exception):
+        dec.rollout([[1] * 270], 1, cache, None, pool=wide)
+    assert wide.pool.cpu().tolist() == [0, 8] and wide.owned.item() == 0 and (wide.table == -1).all()
+    ids, lp = dec.rollout(prompts, n_gen, cache, None, pool=pool, **kw)
+    bt = dec.block_table(B, mb, seed=4)
+    ids_t, lp_t = dec.rollout(prompts, n_gen, dec.alloc_cache(B * mb), bt, **kw)
+    assert torch.equal(ids, ids_t) and same_bits(lp, lp_t)
+    assert bi.bi_device_status() == 0
