@@ -309,6 +309,8 @@ class Decoder:
         if pool is not None and (pool.n_seq != B or pool.n_blocks > cache.n_blocks):
             raise ValueError(f"the pool must be one of {B} sequences and at most {cache.n_blocks} blocks")
         lens = np.array([len(p) for p in prompts])
+        if (sampling is not None or pool is not None) and (lens.min() < 1 or n_gen < 1):
+            raise ValueError("every prompt needs a token, and n_gen must be positive")
         max_ctx = int(lens.max()) + n_gen
         if pool is not None:
             if n_gen > 1 and -(-max_ctx // 64) > pool.max_blocks:

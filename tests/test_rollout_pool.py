@@ -51,6 +51,17 @@ def test_damaged_pools_are_refused():
         _refused(pool, [3, 4], 2, "pool")
 
 
+def test_prompts_without_a_token_are_refused():
+    _refused(_pool(2, 4, 8), [3, 0], 4, "token")
+    _refused(_pool(2, 4, 8), [3, 1], 0, "n_gen")
+    dec = object.__new__(Decoder)
+    dec.device = torch.device("cpu")
+    for lens, n_gen, match in (([3, 0], 4, "token"), ([3, 1], 0, "n_gen")):
+        with pytest.raises(ValueError, match=match):          # drawn without a pool
+            dec.rollout([[1] * n for n in lens], n_gen, KVCache(None, None, 8), None, sampling=bi.bi_sampling(),
+                        uniforms=torch.zeros(n_gen, 2))
+
+
 def test_what_the_check_lets_through_is_served():
     """Random pools against the planning oracle run step by step: served throughout iff the check says so."""
     rng = np.random.default_rng(3)
