@@ -35,10 +35,12 @@
 //    first few by index are counted out.
 // The draw finds the CTA, then the warp, then the token whose running mass crosses u S.
 //
-// What bounds it.  Large batches: instruction issue, not memory.  Reading the logits once would take 39 us for
+// What bounds it.  Large batches: the chain of a CTA's own passes (read, barrier, masses from L2, barrier) with two
+// CTAs an SM to overlap; neither memory nor issue is full (HBM at 42 % and issue 42 % active at temperature alone,
+// issue 53 % with top-p).  Reading the logits once would take 39 us for
 // 512 fp32 rows of 129280 and 78 us for 2048 bf16 rows of them or 4096 fp32 rows of 32000.  At temperature
-// alone the calls take 96, 244 and 164 us (23 instructions a logit), with top_k 178 us for the bf16 rows (the second
-// pass only compares), with top-p 486 and 378 us for the last two: 49 instructions a logit (12 of them the counts, two
+// alone the calls take 96, 242 and 168 us (23 instructions a logit), with top_k 180 us for the bf16 rows (the second
+// pass only compares), with top-p 492 and 378 us for the last two: 49 instructions a logit (12 of them the counts, two
 // shared atomics among them), 24,000 warp instructions a row beside them, and a dozen barriers.  Small calls: that
 // chain alone, 12.0 us for one row of 4096 with top-k (launch and exit are 2.5 of them), 14.5 us for 16 rows of
 // 129280 at temperature alone, 29 us with top-p.  The last way costs a row of 129280 some 180 us.  Measured and
@@ -1558,12 +1560,13 @@ static bi_status launch_sample(const SampleArgs& a, int64_t T, cudaStream_t st) 
 template <typename TL>
 static bi_status dispatch_sample_as(SampleArgs& a, int64_t T, cudaStream_t st) {
   // Bits do not depend on the split.  A row is split while the rows alone leave CTA slots (two per SM) idle, down to
-  // 2K logits a CTA: 64 rows of 129280 with top-k and top-p took 33, 27, 22 and 31 us on 1, 2, 4 and 8 CTAs a row (4 is
-  // the rule's), and 4096 rows of 32000 at temperature alone 185 us on one and 303 us on two (1 is).
+  // 2K logits a CTA: 64 rows of 129280 with top-k and top-p take 25, 23, 22 and 30 us on 1, 2, 4 and 8 CTAs a row (4 is
+  // the rule's), and 4096 rows of 32000 at temperature alone 168 us on one and 281 us on two (1 is).  The rule does not
+  // always find the best: 37 bf16 rows of 50261 under mixed rules take 27 us on its 8, 23 us on 4.
   int cs = 1;
   while (cs < 8 && cdiv(a.V, cs) > 2048 && T * cs * 2 <= 2 * num_sms()) cs *= 2;
   // The rows in flight have to stay in L2 until their last pass: a row of more than 256 KB is split too (512 fp32 rows
-  // of 129280 at temperature alone: 112 us unsplit, 100 us on two CTAs).
+  // of 129280 at temperature alone: 103 us unsplit, 98 us on two CTAs).
   if (cs == 1 && a.V * (int64_t)sizeof(TL) > 256 * 1024) cs = a.V * (int64_t)sizeof(TL) > 512 * 1024 ? 4 : 2;
   a.share = (int)(cdiv(cdiv(a.V, cs), 8) * 8);
   switch (cs) {
