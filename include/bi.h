@@ -160,6 +160,58 @@ bi_status bi_qkv_rope_kv_write(const void* x, int64_t T, int64_t K, const void* 
  * angles and functions evaluated in fp64 on the device, rounded to fp32. */
 bi_status bi_rope_table(float* rope_table, int64_t max_pos, int hd, double theta, void* stream);
 
+/* A RoPE table whose angles are scaled for contexts longer than those trained on.
+ * rope_table fp32 [max_pos, rot]: A cos(p w_i) for i < rot/2 in the first half of
+ * each row, A sin(p w_i) in the second; A = amplitude.  With w_i = theta^(-2i/rot):
+ *   BI_ROPE_PLAIN  w_i
+ *   BI_ROPE_LINEAR w_i / factor (positions interpolated)
+ *   BI_ROPE_BASE   w_i of the base theta * factor^(rot / (rot - 2))
+ *   BI_ROPE_TURNS  w_i (g + (1 - g) / factor), g = clamp((t_i - low) / (high - low),
+ *                  0, 1), t_i = orig_len w_i / (2 pi): pairs that turn often over
+ *                  the orig_len positions of training keep their angle
+ *   BI_ROPE_DIMS   w_i (1 - r + r / factor), r rising from 0 to 1 over the pairs
+ *                  i = floor(d(high)) .. ceil(d(low)) (kept within 0 .. rot - 1),
+ *                  d(t) = rot ln(orig_len / (2 pi t)) / (2 ln theta)
+ * A NULL scaling is BI_ROPE_PLAIN with amplitude 1.  Entries are within 0.6 units
+ * in the last place of |A|, or an angle error of p 2^-52 w_i where that is more,
+ * and within one unit of bi_rope_table's (not always its bits).  A decoder uses
+ * such a table when its caller overwrites bi_weights.rope_table after
+ * bi_model_create.  rot even, 2 <= rot <= 256; theta > 1; max_pos <= 2^31. */
+typedef enum {
+  BI_ROPE_PLAIN = 0,
+  BI_ROPE_LINEAR = 1,
+  BI_ROPE_BASE = 2,
+  BI_ROPE_TURNS = 3,
+  BI_ROPE_DIMS = 4
+} bi_rope_kind;
+typedef struct {
+  int64_t kind;
+  double factor;    /* > 0; not read by BI_ROPE_PLAIN */
+  double orig_len;  /* BI_ROPE_TURNS, BI_ROPE_DIMS: > 0 */
+  double low, high; /* the same: 0 < low < high, in turns */
+  double amplitude;
+} bi_rope_scaling;
+bi_status bi_rope_scaled_table(float* rope_table, int64_t max_pos, int rot, double theta,
+                               const bi_rope_scaling* scaling, void* stream);
+
+/* Rotation of q and k with a K/V write at given slots: row t of qkv (bf16, (Hq +
+ * 2 Hkv) hd values: q heads, k heads, v heads; rows ld elements apart) is rotated
+ * by row row_pos[t] of rope_table (fp32 [max_pos, rot]) and written as
+ * bi_rope_kv_write does, to q_out bf16 [T, Hq, hd] and to cache slot slots[t]
+ * (int64: block * 64 + offset, as bi_slot_map and bi_tree_slot_map give them), so
+ * that a row need not stand at its position.  rot <= hd: the first rot elements of
+ * a head are rotated, the others pass (rot = 0: all); layout BI_ROPE_HALF pairs
+ * (i, i + rot/2), BI_ROPE_INTERLEAVED pairs (2i, 2i + 1).  With BI_ROPE_HALF and
+ * rot = hd the bits are bi_rope_kv_write's.  A position outside [0, max_pos) skips
+ * its row, a slot outside [0, 64 n_blocks) its K and V; both set the device status.
+ * Two rows of a call must not have the same slot.  hd a multiple of 8 (at most
+ * 1024), rot of 16 (BI_ROPE_HALF) or 8, ld of 8; pointers 16-byte aligned (row_pos
+ * and slots to their type). */
+enum { BI_ROPE_HALF = 0, BI_ROPE_INTERLEAVED = 1 };
+bi_status bi_rope_slot_write(const void* qkv, int64_t T, int64_t ld, const int32_t* row_pos, const int64_t* slots,
+                             int Hq, int Hkv, int hd, int rot, int layout, const float* rope_table, int64_t max_pos,
+                             int64_t n_blocks, void* q_out, void* k_cache, void* v_cache, void* stream);
+
 /* ------------------------------------------------- paged-cache planning
  * [Article] §4.2 (every phase writes and reads K/V through the block table),
  * §4.6 (a captured step reads nothing back to the host).
@@ -262,6 +314,74 @@ bi_status bi_attention_static_scratch(const void* q, int64_t T, const int32_t* p
                                       int hd, const void* k_cache, const void* v_cache, const int32_t* block_table,
                                       int64_t max_blocks_per_seq, int64_t n_blocks, int64_t max_ctx, int kv_split,
                                       float scale, void* out, int mode, void* stream);
+
+/* ----------------------------------------------------------- drafted trees
+ * [Article] §2 (the same discrete choices, batch independence), §4.2 (one read
+ * path).  A step may send a tree of drafted tokens per sequence instead of one
+ * token.  Sequence b's nodes are rows row0[b] .. row0[b + 1] - 1 (device int32
+ * [B + 1]); parent[row] (device int32 [T]) is the index, within the sequence, of
+ * the node's parent, which stands before it, or -1 for a root.  The cache holds
+ * start[b] tokens of the sequence before the step (device int32 [B]); node i's key
+ * and value stand at cache position start[b] + i, its own position is start[b] +
+ * its depth (a root: 0).  At most max_nodes (<= 256) nodes a sequence.
+ *
+ * A step: bi_tree_slot_map; per layer the projections with bi_rope_slot_write and
+ * bi_tree_attention; the token chosen at each node (bi_sample or the argmax of
+ * bi_lm_head_logprob); bi_tree_accept.  A node whose path is the sequence's true
+ * continuation has the bits that plain decode steps give it, so the accepted
+ * tokens and their logprobs are those of a rollout without drafts.
+ *
+ * bi_tree_slot_map: the rows of such a step, as bi_slot_map gives them for plain
+ * ones: row0 from n_nodes [B], and per row the sequence, the position (start +
+ * depth) and the cache slot of position start + node.  A node whose parent does
+ * not stand before it, or is below -1, and its descendants have position -1; a
+ * cache position without a block has slot -1; both set the device status, as does
+ * a sequence whose count is below 0 (taken as 0), above max_nodes, or whose rows
+ * go past T: its rows are left as they were.  row_seq, row_pos, slots: NULL where
+ * not wanted (block_table may be NULL without slots).  Rows behind the last
+ * sequence's stay as they were. */
+bi_status bi_tree_slot_map(const int32_t* parent, const int32_t* n_nodes, const int32_t* start, int64_t B,
+                           int64_t max_nodes, const int32_t* block_table, int64_t max_blocks_per_seq, int64_t n_blocks,
+                           int64_t T, int32_t* row0, int32_t* row_seq, int32_t* row_pos, int64_t* slots, void* stream);
+/* bi_tree_attention: row (node, q head h) attends to positions 0 .. start - 1 of
+ * its sequence and to the nodes of its path, itself included, through kv head
+ * h / (Hq/Hkv); no other node matters to it, whatever its key and value hold.  The
+ * arithmetic, splits and types are bi_attention's (BI_INVARIANT) with the path's
+ * nodes at positions start .. start + depth, so a row has the bits that
+ * bi_attention gives for a cache holding just its path.  q bf16 [T, Hq, hd]; out
+ * bf16 [T, Hq * hd]; caches, block_table (row b for sequence b), kv_split and scale
+ * as in bi_attention, kv_split <= 16384; hd in {64, 128}, 64 % (Hq/Hkv) == 0.
+ * max_ctx bounds start + depth + 1.  workspace: bi_tree_attention_workspace_size
+ * bytes.  Rows of an invalid node, of one beyond max_ctx's last split, and of a
+ * sequence whose start is below 0 or whose nodes go past its block table are
+ * zeros and set the device status; a sequence with more than max_nodes nodes or
+ * with rows outside [0, T) writes nothing and sets it; a block id outside
+ * [0, n_blocks) reads as zeros and sets it.  Rows behind the last sequence's stay
+ * as they were.  One schedule (no mode argument). */
+bi_status bi_tree_attention(const void* q, int64_t T, const int32_t* parent, const int32_t* row0, const int32_t* start,
+                            int64_t B, int64_t max_nodes, int Hq, int Hkv, int hd, const void* k_cache,
+                            const void* v_cache, const int32_t* block_table, int64_t max_blocks_per_seq,
+                            int64_t n_blocks, int64_t max_ctx, int kv_split, float scale, void* workspace,
+                            size_t ws_bytes, void* out, void* stream);
+size_t bi_tree_attention_workspace_size(int64_t max_T, int Hq, int hd, int64_t max_ctx, int kv_split);
+/* bi_tree_accept: node 0 (a root: the sequence's last token) is accepted, then,
+ * while there is one, the first child of the last accepted node whose token
+ * (tokens [T]) is the one chosen there (targets [T]).  limit (device int32 [B] or
+ * NULL) and max_path bound the number of accepted nodes.  n_out [B]: that number
+ * m; path [B, max_path]: their indices; tokens_out [B, max_path]: the tokens
+ * chosen at them, i.e. the step's new tokens, the last of which is the next
+ * step's root; -1 behind both; pos_out [B] (apart from start): start + m.  With
+ * caches (bf16 [n_layers, n_blocks, Hkv, 64, hd]; both or neither NULL) the j-th
+ * accepted node's key and value move from position start + path[j] to start + j
+ * in every layer.  A sequence without nodes, with a limit below 1, whose node 0 is
+ * no root, or whose rows or start are out of range (device status) accepts none; a
+ * node whose parent is not before it is no child (device status); a row whose
+ * block is outside [0, n_blocks) does not move (device status). */
+bi_status bi_tree_accept(const int32_t* parent, const int32_t* row0, const int32_t* start, const int32_t* tokens,
+                         const int32_t* targets, const int32_t* limit, int64_t B, int64_t max_nodes, int64_t T,
+                         int64_t max_path, int32_t* n_out, int32_t* path, int32_t* tokens_out, int32_t* pos_out,
+                         int64_t n_layers, int Hkv, int hd, void* k_cache, void* v_cache, const int32_t* block_table,
+                         int64_t max_blocks_per_seq, int64_t n_blocks, void* stream);
 
 /* ------------------------------------------------------------- block FP8
  * [Article] §4.1 ("Dense GEMM: keep FP8, one accumulation order for every M"):

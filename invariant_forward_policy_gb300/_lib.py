@@ -24,6 +24,9 @@ BI_DTYPE_BF16 = 0
 BI_DTYPE_FP32 = 1
 BI_EPI_NONE = 0
 BI_EPI_SWIGLU = 1
+BI_ROPE_PLAIN, BI_ROPE_LINEAR, BI_ROPE_BASE, BI_ROPE_TURNS, BI_ROPE_DIMS = range(5)
+BI_ROPE_HALF = 0
+BI_ROPE_INTERLEAVED = 1
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libbi.so")
 
@@ -58,6 +61,14 @@ class bi_weights(ctypes.Structure):
                 ("rope_table", _vp)]
 
 
+class bi_rope_scaling(ctypes.Structure):
+    _fields_ = [("kind", _i64), ("factor", _f64), ("orig_len", _f64), ("low", _f64), ("high", _f64),
+                ("amplitude", _f64)]
+
+    def __init__(self, kind=BI_ROPE_PLAIN, factor=1.0, orig_len=1.0, low=1.0, high=2.0, amplitude=1.0):
+        ctypes.Structure.__init__(self, kind, factor, orig_len, low, high, amplitude)
+
+
 class bi_sampling(ctypes.Structure):
     """Sampling parameters: device tensors of n entries each (fp32, int32 for top_k), or None."""
     _fields_ = [("temperature", _vp), ("top_k", _vp), ("top_p", _vp), ("min_p", _vp), ("n", _i64)]
@@ -90,6 +101,15 @@ _SIGS = {
     "bi_rope_kv_write": (_int, [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _int, _int, _int, _vp, _i64, _vp, _i64, _i64,
                                 _vp, _vp, _vp, _vp]),
     "bi_rope_table": (_int, [_vp, _i64, _int, _f64, _vp]),
+    "bi_rope_scaled_table": (_int, [_vp, _i64, _int, _f64, ctypes.POINTER(bi_rope_scaling), _vp]),
+    "bi_rope_slot_write": (_int, [_vp, _i64, _i64, _vp, _vp, _int, _int, _int, _int, _int, _vp, _i64, _i64, _vp, _vp,
+                                  _vp, _vp]),
+    "bi_tree_slot_map": (_int, [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "bi_tree_attention": (_int, [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _int, _int, _int, _vp, _vp, _vp, _i64, _i64,
+                                 _i64, _int, _f32, _vp, _sz, _vp, _vp]),
+    "bi_tree_attention_workspace_size": (_sz, [_i64, _int, _int, _i64, _int]),
+    "bi_tree_accept": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _int,
+                              _int, _vp, _vp, _vp, _i64, _i64, _vp]),
     "bi_qkv_rope_kv_write": (_int, [_vp, _i64, _i64, _vp, _int, _int, _int, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _vp,
                                     _vp, _vp, _int, _vp]),
     "bi_block_table_resize": (_int, [_vp, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp]),
@@ -257,6 +277,46 @@ def bi_qkv_rope_kv_write(x, T, K, wqkv, Hq, Hkv, hd, row_seq, row_pos, rope_tabl
 
 def bi_rope_table(table, max_pos, hd, theta=10000.0, stream=None):
     _check(load().bi_rope_table(_p(table), max_pos, hd, theta, _s(stream)))
+
+
+def bi_rope_scaled_table(table, max_pos, rot, theta=10000.0, scaling=None, stream=None):
+    """scaling: a bi_rope_scaling, or None for the plain table."""
+    _check(load().bi_rope_scaled_table(_p(table), max_pos, rot, theta, scaling, _s(stream)))
+
+
+def bi_rope_slot_write(qkv, T, row_pos, slots, Hq, Hkv, hd, rope_table, max_pos, n_blocks, q_out, k_cache, v_cache,
+                       rot=None, layout=BI_ROPE_HALF, ld=None, stream=None):
+    """rot: the whole head unless given; ld: rows without a gap unless given."""
+    _check(load().bi_rope_slot_write(_p(qkv), T, (Hq + 2 * Hkv) * hd if ld is None else ld, _p(row_pos), _p(slots), Hq,
+                                     Hkv, hd, hd if rot is None else rot, layout, _p(rope_table), max_pos, n_blocks,
+                                     _p(q_out), _p(k_cache), _p(v_cache), _s(stream)))
+
+
+def bi_tree_slot_map(parent, n_nodes, start, B, max_nodes, block_table, max_blocks_per_seq, n_blocks, T, row0,
+                     row_seq=None, row_pos=None, slots=None, stream=None):
+    _check(load().bi_tree_slot_map(_p(parent), _p(n_nodes), _p(start), B, max_nodes, _p(block_table),
+                                   max_blocks_per_seq, n_blocks, T, _p(row0), _p(row_seq), _p(row_pos), _p(slots),
+                                   _s(stream)))
+
+
+def bi_tree_attention(q, T, parent, row0, start, B, max_nodes, Hq, Hkv, hd, k_cache, v_cache, block_table,
+                      max_blocks_per_seq, n_blocks, max_ctx, kv_split, scale, workspace, out, stream=None):
+    _check(load().bi_tree_attention(_p(q), T, _p(parent), _p(row0), _p(start), B, max_nodes, Hq, Hkv, hd, _p(k_cache),
+                                    _p(v_cache), _p(block_table), max_blocks_per_seq, n_blocks, max_ctx, kv_split,
+                                    scale, _p(workspace), _nb(workspace), _p(out), _s(stream)))
+
+
+def bi_tree_attention_workspace_size(max_T, Hq, hd, max_ctx, kv_split) -> int:
+    return load().bi_tree_attention_workspace_size(max_T, Hq, hd, max_ctx, kv_split)
+
+
+def bi_tree_accept(parent, row0, start, tokens, targets, B, max_nodes, T, max_path, n_out, path, tokens_out, pos_out,
+                   limit=None, n_layers=0, Hkv=0, hd=0, k_cache=None, v_cache=None, block_table=None,
+                   max_blocks_per_seq=0, n_blocks=0, stream=None):
+    """Without caches only the path is found; with them its keys and values move to where the sequence goes on."""
+    _check(load().bi_tree_accept(_p(parent), _p(row0), _p(start), _p(tokens), _p(targets), _p(limit), B, max_nodes, T,
+                                 max_path, _p(n_out), _p(path), _p(tokens_out), _p(pos_out), n_layers, Hkv, hd,
+                                 _p(k_cache), _p(v_cache), _p(block_table), max_blocks_per_seq, n_blocks, _s(stream)))
 
 
 def bi_rope_kv_write(qkv, T, piece_seq, piece_row0, piece_pos0, P, max_q_len, Hq, Hkv, hd, rope_table, max_pos,
