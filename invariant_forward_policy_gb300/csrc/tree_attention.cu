@@ -7,16 +7,16 @@
 // that holds just that path (splits, lanes, 64-key tiles and 16-key MMA steps by position), so it has the bits
 // that a plain decode of the path gives.
 //
-// What bounds it: keys and values are read once for a tile of up to 64 query rows (nodes x q heads of a group),
-// so small trees are bound by HBM, large ones by mma.sync and the shared-memory reads that feed it.
 //
-// A CTA owns (sequence, row tile, kv head, split).  The keys before `start` are the same for all rows: whole 64-key
-// pages come by TMA into a ring and every warp runs its 16 rows over them.  Tiles that hold positions from
-// `start` on differ by node: the pages that hold the tree's own keys are then all in the ring at once, and a
-// node's tile is read by ldmatrix with a row address for each position (the page's row for a position before
-// `start`, the path node's row behind it).  An 8-key group of scores or a 16-key step of P V whose positions all
-// stand before `start` is done for the warp's 16 rows at once; the others once for each node of the warp, and a
-// row keeps its own node's result.
+// Three launches.  Let E be the start of the lane (of bi_attention's partition) that holds position `start`.
+//   * tree_tail_kernel: the lanes from E on, which differ by node, on mma.sync; a record (m, l, acc) for each row
+//     and lane.
+//   * tree_context_kernel: the lanes before E, which every node of a sequence sees whole, on tcgen05; a record for
+//     each row and split.  It needs nothing of the tail kernel and runs beside it.
+//   * tree_merge_kernel: folds and merges a row's records in order.
+// What bounds it: a page of keys and values is read once for up to 128 query rows (nodes x q heads of a group), so
+// HBM bounds small trees; with more rows the softmax's instructions and the split records (one for every 512
+// positions of every row: as many bytes as the keys and values themselves at 256 rows) do.
 #include <algorithm>
 #include <mutex>
 #include <string>
@@ -31,14 +31,18 @@ namespace bi {
 struct TreeArgs {
   const __nv_bfloat16* q;  // [T, Hq, hd]
   const int32_t *parent, *row0, *start, *block_table;
-  float* part_o;    // [T, Hq, nsplit, hd]
+  float* part_o;    // [T, Hq, nsplit, hd]: the lanes before E
   float* part_ml;   // [T, Hq, nsplit, 2]
+  float* tail_o;    // [T, Hq, ntail, hd]: the lanes from E on, one by one
+  float* tail_ml;   // [T, Hq, ntail, 2]
   int32_t* row_pos; // [T]: a node's position, -1 when it has none
+  const void *k_cache, *v_cache;
   __nv_bfloat16* out;
   int* status;
   int64_t T, max_blk, n_blocks;
-  int max_nodes, Hq, Hkv, group, nsplit, split, stages;
+  int max_nodes, Hq, Hkv, group, nsplit, ntail, split, lane_len, stages, per_cta;
   float scale_log2;
+  float neg_zero;  // -0, see mul2
 };
 
 constexpr int kTreeMaxSplit = 16384;  // positions of a split: 256 pages, whose ids stand in shared memory
@@ -53,13 +57,23 @@ struct TreeSeq {
 };
 BI_DEV TreeSeq tree_seq(const TreeArgs& a, int b) {
   TreeSeq s;
-  const int64_t r0 = a.row0[b], r1 = a.row0[b + 1];
+  const int64_t r0 = __ldcg(a.row0 + b), r1 = __ldcg(a.row0 + b + 1);
   s.row0 = r0;
-  s.start = a.start[b];
+  s.start = __ldcg(a.start + b);
   s.rows_ok = r0 >= 0 && r1 >= r0 && r1 <= a.T && r1 - r0 <= a.max_nodes;
   s.n = s.rows_ok ? (int)(r1 - r0) : 0;
   s.ok = s.rows_ok && s.start >= 0 && (int64_t)s.start + s.n <= a.max_blk * kKeys;
   return s;
+}
+
+// E: the start of the lane that holds position `start`.
+BI_DEV int tail_lane(const TreeArgs& a, int start) {
+  const int kv = start / a.split * a.split;
+  return kv + (start - kv) / a.lane_len * a.lane_len;
+}
+// The end of the lane that begins at `at`.
+BI_DEV int lane_end(const TreeArgs& a, int at) {
+  return min(at + a.lane_len, (at / a.split + 1) * a.split);
 }
 
 template <int HD>
@@ -136,33 +150,39 @@ __device__ __forceinline__ void tree_pv(uint32_t sv, const float (&p)[8][4], int
   }
 }
 
-// Shared memory: the page ring, then barriers, a row of zeros, depths, parents, the warps' path
-// tables and the page ids of the CTA.
-template <int HD, int WARPS>
-struct TreeLayout {
+// ------------------------------------------------------------------------ the lanes from E on
+// A CTA owns (sequence, tile of 64 rows, kv head).  Pages come by TMA into a ring.  The few pages before position
+// `start` count for every row and are run over by every warp's 16 rows.  Tiles that hold positions from `start` on
+// differ by node: the pages that hold the tree's own keys are then all in the ring at once, and a node's tile is
+// read by ldmatrix with a row address for each position (the page's row for a position before `start`, the path
+// node's row behind it).  An 8-key group of scores or a 16-key step of P V whose positions all stand before `start`
+// is done for the warp's 16 rows at once, the others once for each node of the warp; a row keeps its own node's
+// result, so no other node's key or value reaches it.
+constexpr int kTailWarps = 4;
+
+// Shared memory: the page ring, then barriers, a row of zeros, depths, parents and the warps' path tables.
+template <int HD>
+struct TailLayout {
   static constexpr int kPage = kKeys * HD * 2;
   static constexpr int kStage = 2 * kPage;  // a K page and its V page
   static constexpr int kMaxStages = 12;
   static constexpr int kZero = HD * 2;      // a key row of zeros
-  static int ids(int split) { return (split / kKeys + kMaxTreeNodes / kKeys + 2) * 4; }
-  static int bytes(int stages, int split) {
-    return 1024 + stages * kStage + 256 + kZero + kMaxTreeNodes * 4 + WARPS * 16 * kKeys * 2 + ids(split);
+  static int bytes(int stages) {
+    return 1024 + stages * kStage + 256 + kZero + kMaxTreeNodes * 4 + kTailWarps * 16 * kKeys * 2;
   }
 };
 
-// ROWS: 16-row warps of a row tile.  LANES: the split's four lanes on warps of their own (few rows: more warps to
-// hide latency with), or 1: one after another.
-template <int HD, int ROWS, int LANES>
-__global__ void __launch_bounds__(ROWS * LANES * 32) tree_attention_kernel(const TreeArgs a,
-                                                                           const __grid_constant__ CUtensorMap tmk,
-                                                                           const __grid_constant__ CUtensorMap tmv) {
-  constexpr int WARPS = ROWS * LANES;
-  using Lay = TreeLayout<HD, WARPS>;
+template <int HD>
+__global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(const TreeArgs a,
+                                                                    const __grid_constant__ CUtensorMap tmk,
+                                                                    const __grid_constant__ CUtensorMap tmv) {
+  using Lay = TailLayout<HD>;
+  constexpr int WARPS = kTailWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int NS = a.stages;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + NS * Lay::kStage);  // [NS] the stage's pages have landed
-  uint64_t* empty = full + Lay::kMaxStages;                               // [NS] its warps have read them
+  uint64_t* empty = full + Lay::kMaxStages;                               // [NS] the warps have read them
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + Lay::kMaxStages);
   int* max_depth = const_cast<int*>(abort_flag) + 1;
   volatile int* issued = abort_flag + 2;  // [NS] the page that was last asked for in each stage
@@ -170,95 +190,49 @@ __global__ void __launch_bounds__(ROWS * LANES * 32) tree_attention_kernel(const
   int16_t* depth_of = reinterpret_cast<int16_t*>(zero_row + Lay::kZero);
   int16_t* parent_of = depth_of + kMaxTreeNodes;
   uint16_t* paths = reinterpret_cast<uint16_t*>(parent_of + kMaxTreeNodes);  // [WARPS][16][64]
-  int32_t* ids = reinterpret_cast<int32_t*>(paths + WARPS * 16 * kKeys);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b = blockIdx.y;
-  const int kvh = (int)blockIdx.z % a.Hkv, s = (int)blockIdx.z / a.Hkv;
+  const int b = blockIdx.y, kvh = blockIdx.z;
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], ROWS);
+      mbar_init(&empty[i], WARPS);
       issued[i] = -1;
     }
     *abort_flag = 0;
-    *max_depth = -1;
     fence_barrier_init();
   }
   for (int i = tid; i < Lay::kZero / 4; i += WARPS * 32) reinterpret_cast<uint32_t*>(zero_row)[i] = 0u;
-  pdl_trigger();
+  // the context kernel reads what this kernel's predecessors wrote without waiting for this one: it may start only
+  // once they have completed
   pdl_wait();
+  pdl_trigger();
   const TreeSeq sq = tree_seq(a, b);
-  const bool speaks = s == 0 && kvh == 0;  // the CTA that reports its sequence's faults and writes positions
+  const bool speaks = kvh == 0;  // reports the sequence's faults and writes positions
   const int n = sq.n, start = sq.start;
-  const int node0 = (int)((int64_t)blockIdx.x * ROWS * 16 / a.group);  // the tile's first node
-  if (speaks && tid == 0 && !sq.ok) report(a.status, DEV_BAD_INDEX);
+  const int64_t r_first = (int64_t)blockIdx.x * WARPS * 16;  // the tile's first row of the sequence's n * group
+  const int node0 = (int)(r_first / a.group);
+  if (speaks && blockIdx.x == 0 && tid == 0 && !sq.ok) report(a.status, DEV_BAD_INDEX);
   if (node0 >= n) return;
-  const int last_node = min(n, (int)(((int64_t)(blockIdx.x + 1) * ROWS * 16 + a.group - 1) / a.group)) - 1;
+  const int last_node = min(n, (int)((r_first + WARPS * 16 + a.group - 1) / a.group)) - 1;
   if (!sq.ok) {
     if (speaks)
       for (int i = node0 + tid; i <= last_node; i += WARPS * 32) a.row_pos[sq.row0 + i] = -1;
     return;
   }
-  const int kv_begin = s * a.split;
-  // no position of this split is at or before any row's
-  if (kv_begin > start + last_node) return;
-  const int lane_len = ((a.split + 3) / 4 + kKeys - 1) / kKeys * kKeys;
-  const int tail0 = start / kKeys * kKeys;  // the first tile with positions from `start` on
-  // depths (and so the rows' own positions) matter to splits that reach such a tile, and to whoever writes them down
-  const bool tail = kv_begin + a.split > tail0;
-  const int n_plain = max(0, min(kv_begin + a.split, tail0) - kv_begin) / kKeys;
-  const int tail_page0 = start / kKeys;
-  const int tail_pages = tail ? (start + last_node) / kKeys - tail_page0 + 1 : 0;
-  const int n_pages = n_plain + tail_pages;
-  for (int i = tid; i < n_pages; i += WARPS * 32) {
-    const int page = i < n_plain ? kv_begin / kKeys + i : tail_page0 + i - n_plain;
-    ids[i] = page < a.max_blk ? a.block_table[(int64_t)b * a.max_blk + page] : -1;
-  }
-  if ((tail || speaks) && warp == WARPS - 1) {
-    const bool bad = tree_depths(a.parent + sq.row0, last_node + 1, depth_of, lane, parent_of);
-    int deep = -1;
-    bool far = false;
-    for (int i = node0 + lane; i <= last_node; i += 32) {
-      const int d = depth_of[i];
-      const bool fits = (int64_t)start + d < (int64_t)a.nsplit * a.split;
-      far |= !fits;
-      if (d >= 0 && fits) deep = max(deep, d);
-      if (speaks) a.row_pos[sq.row0 + i] = d >= 0 && fits ? start + d : -1;
-    }
-    for (int o = 16; o; o >>= 1) deep = max(deep, __shfl_xor_sync(0xffffffffu, deep, o));
-    if (lane == 0) *max_depth = deep;
-    if (speaks && (bad || far)) report(a.status, DEV_BAD_INDEX);
-  }
-  __syncthreads();
-  const int deep = tail ? *max_depth : 0;
-  // logical tiles from tail0 on that some row of the tile sees in this split
-  const int tail_begin = max(tail0, kv_begin);
-  const int tail_end = tail ? min(kv_begin + a.split, start + deep + 1) : 0;
-  if (n_plain == 0 && tail_end <= tail_begin) return;
-  const int n_issue = tail_end > tail_begin ? n_pages : n_plain;
-
-  // plain pages in the order in which they are used: round k holds page k of every lane that has one
-  const int ppl = lane_len / kKeys;
-  const int nl = (n_plain + ppl - 1) / ppl;
-  const int last_cnt = n_plain - (nl - 1) * ppl;  // pages of the last lane
-  auto order_of = [&](int ln, int k) {
-    return LANES == 1 ? ln * ppl + k : (k < last_cnt ? k * nl + ln : last_cnt * nl + (k - last_cnt) * (nl - 1) + ln);
-  };
-  auto page_at = [&](int j) {
-    if (LANES == 1 || j >= n_plain) return j;
-    if (j < last_cnt * nl) return j % nl * ppl + j / nl;
-    const int r = j - last_cnt * nl;
-    return r % (nl - 1) * ppl + last_cnt + r / (nl - 1);
-  };
+  const int E = tail_lane(a, start);
+  const int tail_page0 = start / kKeys, tail0 = tail_page0 * kKeys;
+  const int n_plain = (tail0 - E) / kKeys;  // whole pages of the first lane before `start`
+  const int tail_pages = (start + last_node) / kKeys - tail_page0 + 1;
+  const int n_issue = n_plain + tail_pages;
   const int rows_total = (int)(a.n_blocks * a.Hkv * kKeys);
   auto issue = [&](int j) {
-    const int32_t id = ids[page_at(j)];
+    const int page = E / kKeys + j;
+    const int32_t id = page < a.max_blk ? __ldcg(a.block_table + (int64_t)b * a.max_blk + page) : -1;
     int row = rows_total;  // past the end: the copy reads zeros
     if (id >= 0 && id < a.n_blocks) row = (int)(((int64_t)id * a.Hkv + kvh) * kKeys);
     else report(a.status, DEV_BAD_INDEX);
     const int slot = j % NS;
     uint8_t* sk = smem + slot * Lay::kStage;
-    __threadfence_block();
     issued[slot] = j;
     mbar_arrive_expect_tx(&full[slot], Lay::kStage);
 #pragma unroll
@@ -269,21 +243,35 @@ __global__ void __launch_bounds__(ROWS * LANES * 32) tree_attention_kernel(const
   };
   if (tid == 0)
     for (int j = 0; j < NS && j < n_issue; ++j) issue(j);
+  if (warp == WARPS - 1) {
+    const bool bad = tree_depths(a.parent + sq.row0, last_node + 1, depth_of, lane, parent_of);
+    int deep = -1;
+    bool far = false;
+    for (int i = node0 + lane; i <= last_node; i += 32) {
+      const int d = depth_of[i];
+      const bool fits = start + d < a.nsplit * a.split;
+      far |= !fits;
+      if (d >= 0 && fits) deep = max(deep, d);
+      if (speaks) a.row_pos[sq.row0 + i] = d >= 0 && fits ? start + d : -1;
+    }
+    for (int o = 16; o; o >>= 1) deep = max(deep, __shfl_xor_sync(0xffffffffu, deep, o));
+    far = __any_sync(0xffffffffu, far);
+    if (lane == 0) *max_depth = deep;
+    if (speaks && (bad || far)) report(a.status, DEV_BAD_INDEX);
+  }
 
   // this warp's rows: node, q head and position of the two a thread holds
   const int g = lane >> 2, tq = lane & 3;
-  const int rw = warp % ROWS, lw = warp / ROWS;
+  const int64_t wr0 = r_first + warp * 16;
   int row_node[2], row_pos[2], row_head[2];
   bool row_valid[2];
   uint32_t qf[HD / 16][4];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int64_t r = (int64_t)blockIdx.x * ROWS * 16 + rw * 16 + g + h * 8;
+    const int64_t r = wr0 + g + h * 8;
     row_node[h] = (int)(r / a.group);
     row_valid[h] = row_node[h] < n;
     row_head[h] = kvh * a.group + (int)(r % a.group);
-    const int d = row_valid[h] && tail ? depth_of[row_node[h]] : 0;
-    row_pos[h] = row_valid[h] && d >= 0 && start + d < a.nsplit * a.split ? start + d : -1;
     const __nv_bfloat16* qr = a.q + ((sq.row0 + row_node[h]) * a.Hq + row_head[h]) * HD + tq * 2;
 #pragma unroll
     for (int kk = 0; kk < HD / 16; ++kk) {
@@ -291,244 +279,710 @@ __global__ void __launch_bounds__(ROWS * LANES * 32) tree_attention_kernel(const
       qf[kk][2 + h] = row_valid[h] ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8) : 0u;
     }
   }
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int d = row_valid[h] ? depth_of[row_node[h]] : -1;
+    row_pos[h] = d >= 0 && start + d < a.nsplit * a.split ? start + d : -1;
+  }
+  const int end = start + *max_depth + 1;  // behind the last position that a row of the tile sees
 
-  LaneState<HD> cur, run;
-  clear(run);
-  clear(cur);
-  int prev = -1;  // the page (in order of use) that this group of warps read last
   bool ok = true;
-  auto refill = [&]() {  // the freed stage takes the page NS places on
-    if (rw == 0 && lane == 0 && prev >= 0 && prev + NS < n_issue) {
-      if (!mbar_wait(&empty[prev % NS], (prev / NS) & 1)) {
-        report(a.status, DEV_TIMEOUT);
-        *abort_flag = 1;
-      } else {
-        issue(prev + NS);
-      }
-    }
-    prev = -1;
-  };
   auto wait_page = [&](int j) {
-    bool there = true;
-    if constexpr (LANES > 1) {
-      // the stage's page before this one may be another group's, not landed yet: its phase must not be taken for this one's
-      const unsigned long long t0 = globaltimer();
-      while (there && issued[j % NS] != j) there = globaltimer() - t0 < kWaitLimitNs;
-      __threadfence_block();
-    }
-    if (!there || !mbar_wait(&full[j % NS], (j / NS) & 1)) {
+    if (!mbar_wait(&full[j % NS], (j / NS) & 1)) {
       report(a.status, DEV_TIMEOUT);
       *abort_flag = 1;
     }
     return (bool)__all_sync(0xffffffffu, *abort_flag == 0);
   };
-
   uint16_t* path = paths + warp * 16 * kKeys;
   const int per_node = min(a.group, 16);           // rows of a node in this warp
   const int n_slots = 16 / per_node;               // nodes of this warp
-  const int64_t wr0 = (int64_t)blockIdx.x * ROWS * 16 + rw * 16;
   const int wnode0 = (int)(wr0 / a.group);
   const int wlast = min(n, wnode0 + n_slots) - 1;  // the warp's last node
-  bool tail_here = false;
-  const int lanes = (a.split + lane_len - 1) / lane_len;
-  for (int ln = LANES == 1 ? 0 : lw; ok && ln < lanes; ln += LANES) {
-    const int lb = kv_begin + ln * lane_len, le = min(lb + lane_len, kv_begin + a.split);
-    const int plain = max(0, min(ppl, n_plain - ln * ppl));
-    for (int k = 0; ok && k < plain; ++k) {
-      const int j = order_of(ln, k);
-      refill();
-      if (!(ok = wait_page(j))) break;
-      const uint32_t sk = smem_u32(smem + j % NS * Lay::kStage);
-      float sc[8][4];
-      attn_scores<HD, 2>(sk, qf, lane, sc);
-      tree_softmax<HD, false>(sc, 0, row_pos, a.scale_log2, lane, cur);
-      tree_pv<HD>(sk + Lay::kPage, sc, lane, cur);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[j % NS]);
-      prev = j;
-    }
-    // tiles that hold positions from `start` on
-    const int tb = max(lb, tail_begin), te = min(le, tail_end);
-    if (ok && tb < te) {
-      refill();
-      if (!tail_here) {
-        for (int i = 0; ok && i < tail_pages; ++i) ok = wait_page(n_plain + i);
-        tail_here = true;
-        if (!ok) break;
-      }
-      for (int key0 = tb / kKeys * kKeys; key0 < te; key0 += kKeys) {
-        // path[slot][i]: the row, among the tail pages' rows, of position key0 + i (0xffff: none, a row of zeros)
-        __syncwarp();
-        for (int i = lane; i < n_slots * kKeys; i += 32) {
-          const int p = key0 + i % kKeys;
-          path[i] = p < start ? (uint16_t)(p - tail0) : (uint16_t)0xffff;
-        }
-        __syncwarp();
-        if (lane < n_slots && wnode0 + lane <= wlast) {
-          int node = wnode0 + lane;
-          for (int p = start + depth_of[node]; p >= start && p >= key0; --p) {
-            if (p < key0 + kKeys) path[lane * kKeys + p - key0] = (uint16_t)(start - tail0 + node);
-            node = parent_of[node];
-          }
-        }
-        __syncwarp();
-        // byte address of chunk ch of position i of node slot ns; v: of the V page
-        auto addr = [&](int ns, int i, int ch, bool v) -> uint32_t {
-          const int off = path[ns * kKeys + i];
-          if (off == 0xffff) return smem_u32(zero_row) + ch * 16;
-          const int pg = n_plain + off / kKeys;
-          return smem_u32(smem + pg % NS * Lay::kStage + (v ? Lay::kPage : 0)) + kv_off<HD>(off % kKeys, ch);
-        };
-        float sc[8][4];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
-          const bool shared = key0 + j * 8 + 7 < start;
-          for (int ns = 0; ns < (shared ? 1 : n_slots); ++ns) {
-            if (!shared && (wnode0 + ns > wlast || start + depth_of[wnode0 + ns] < key0 + j * 8)) continue;
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int kk = 0; kk < HD / 16; kk += 2) {
-              uint32_t b0, b1, b2, b3;
-              ldsm_x4(addr(ns, j * 8 + (lane & 7), kk * 2 + (lane >> 3), false), b0, b1, b2, b3);
-              mma_bf16_16816(d, qf[kk], b0, b1);
-              mma_bf16_16816(d, qf[kk + 1], b2, b3);
-            }
-            const bool mine0 = shared || g / per_node == ns, mine1 = shared || (g + 8) / per_node == ns;
-            sc[j][0] = mine0 ? d[0] : sc[j][0];
-            sc[j][1] = mine0 ? d[1] : sc[j][1];
-            sc[j][2] = mine1 ? d[2] : sc[j][2];
-            sc[j][3] = mine1 ? d[3] : sc[j][3];
-          }
-        }
-        tree_softmax<HD, true>(sc, key0, row_pos, a.scale_log2, lane, cur);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint32_t pa[4] = {pack_bf16x2(sc[2 * kk][0], sc[2 * kk][1]), pack_bf16x2(sc[2 * kk][2], sc[2 * kk][3]),
-                                  pack_bf16x2(sc[2 * kk + 1][0], sc[2 * kk + 1][1]),
-                                  pack_bf16x2(sc[2 * kk + 1][2], sc[2 * kk + 1][3])};
-          const bool shared = key0 + kk * 16 + 15 < start;
-          for (int ns = 0; ns < (shared ? 1 : n_slots); ++ns) {
-            if (wnode0 + ns > wlast) continue;
-            const bool mine0 = shared || g / per_node == ns, mine1 = shared || (g + 8) / per_node == ns;
-#pragma unroll
-            for (int j = 0; j < HD / 8; j += 2) {
-              const int key = kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
-              uint32_t b0, b1, b2, b3;
-              ldsm_x4_t(addr(ns, key, j + (lane >> 4), true), b0, b1, b2, b3);
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                float (&acc)[4] = cur.acc[j + x];
-                float d[4] = {acc[0], acc[1], acc[2], acc[3]};
-                mma_bf16_16816(d, pa, x ? b2 : b0, x ? b3 : b1);
-                acc[0] = mine0 ? d[0] : acc[0];
-                acc[1] = mine0 ? d[1] : acc[1];
-                acc[2] = mine1 ? d[2] : acc[2];
-                acc[3] = mine1 ? d[3] : acc[3];
-              }
-            }
-          }
-        }
+
+  LaneState<HD> cur;
+  clear(cur);
+  for (int j = 0; ok && j < n_plain; ++j) {
+    if (!(ok = wait_page(j))) break;
+    const uint32_t sk = smem_u32(smem + j % NS * Lay::kStage);
+    float sc[8][4];
+    attn_scores<HD, 2>(sk, qf, lane, sc);
+    tree_softmax<HD, false>(sc, 0, row_pos, a.scale_log2, lane, cur);
+    tree_pv<HD>(sk + Lay::kPage, sc, lane, cur);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[j % NS]);
+    if (tid == 0 && j + NS < n_issue) {  // the freed stage takes the page NS places on
+      if (!mbar_wait(&empty[j % NS], (j / NS) & 1)) {
+        report(a.status, DEV_TIMEOUT);
+        *abort_flag = 1;
+      } else {
+        issue(j + NS);
       }
     }
-    if constexpr (LANES == 1) {  // the finished lane folds into the split's state
-      lane_merge<HD>(run, cur.m, cur.l, cur.acc);
-      clear(cur);
-    }
+    __syncwarp();
   }
-  refill();
-  if constexpr (LANES > 1) {
-    // the lanes meet in shared memory, over the ring, once every warp is through with it
-    __syncthreads();
-    constexpr int NF = 4 + HD / 2;  // floats of a thread's state
-    float* mine = reinterpret_cast<float*>(smem) + warp * NF * 32 + lane;
-    if (*abort_flag == 0) {
-      mine[0] = cur.m[0];
-      mine[32] = cur.m[1];
-      mine[64] = cur.l[0];
-      mine[96] = cur.l[1];
+  for (int i = 0; ok && i < tail_pages; ++i) ok = wait_page(n_plain + i);
+  int lb = E;
+  for (int t = 0; ok && t < a.ntail && lb < end; ++t) {
+    const int le = lane_end(a, lb);
+    for (int key0 = max(lb, tail0); key0 < min(le, end); key0 += kKeys) {
+      // path[slot][i]: the row, among the tail pages' rows, of position key0 + i (0xffff: none, a row of zeros)
+      __syncwarp();
+      for (int i = lane; i < n_slots * kKeys; i += 32) {
+        const int p = key0 + i % kKeys;
+        path[i] = p < start ? (uint16_t)(p - tail0) : (uint16_t)0xffff;
+      }
+      __syncwarp();
+      int wdeep = -1;  // the deepest of the warp's nodes
+      if (lane < n_slots && wnode0 + lane <= wlast) {
+        int node = wnode0 + lane;
+        wdeep = depth_of[node];
+        for (int p = start + wdeep; p >= start && p >= key0; --p) {
+          if (p < key0 + kKeys) path[lane * kKeys + p - key0] = (uint16_t)(start - tail0 + node);
+          node = parent_of[node];
+        }
+      }
+      for (int o = 8; o; o >>= 1) wdeep = max(wdeep, __shfl_xor_sync(0xffffffffu, wdeep, o));
+      wdeep = __shfl_sync(0xffffffffu, wdeep, 0);
+      __syncwarp();
+      // byte address of chunk ch of position i of node slot ns; v: of the V page
+      auto addr = [&](int ns, int i, int ch, bool v) -> uint32_t {
+        const int off = path[ns * kKeys + i];
+        if (off == 0xffff) return smem_u32(zero_row) + ch * 16;
+        const int pg = n_plain + off / kKeys;
+        return smem_u32(smem + pg % NS * Lay::kStage + (v ? Lay::kPage : 0)) + kv_off<HD>(off % kKeys, ch);
+      };
+      float sc[8][4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+        const bool shared = key0 + j * 8 + 7 < start;
+        for (int ns = 0; ns < (shared ? 1 : n_slots); ++ns) {
+          // a node without a position in this group of keys: its scores there are masked
+          if (!shared && (wnode0 + ns > wlast || start + depth_of[wnode0 + ns] < key0 + j * 8)) continue;
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; kk += 2) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4(addr(ns, j * 8 + (lane & 7), kk * 2 + (lane >> 3), false), b0, b1, b2, b3);
+            mma_bf16_16816(d, qf[kk], b0, b1);
+            mma_bf16_16816(d, qf[kk + 1], b2, b3);
+          }
+          const bool mine0 = shared || g / per_node == ns, mine1 = shared || (g + 8) / per_node == ns;
+          sc[j][0] = mine0 ? d[0] : sc[j][0];
+          sc[j][1] = mine0 ? d[1] : sc[j][1];
+          sc[j][2] = mine1 ? d[2] : sc[j][2];
+          sc[j][3] = mine1 ? d[3] : sc[j][3];
+        }
+      }
+      tree_softmax<HD, true>(sc, key0, row_pos, a.scale_log2, lane, cur);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint32_t pa[4] = {pack_bf16x2(sc[2 * kk][0], sc[2 * kk][1]), pack_bf16x2(sc[2 * kk][2], sc[2 * kk][3]),
+                                pack_bf16x2(sc[2 * kk + 1][0], sc[2 * kk + 1][1]),
+                                pack_bf16x2(sc[2 * kk + 1][2], sc[2 * kk + 1][3])};
+        const bool shared = key0 + kk * 16 + 15 < start;
+        for (int ns = 0; ns < (shared ? 1 : n_slots); ++ns) {
+          // P is zero for a node without a position in this step
+          if (!shared && (wnode0 + ns > wlast || start + depth_of[wnode0 + ns] < key0 + kk * 16)) continue;
+          const bool mine0 = shared || g / per_node == ns, mine1 = shared || (g + 8) / per_node == ns;
+#pragma unroll
+          for (int j = 0; j < HD / 8; j += 2) {
+            const int key = kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4_t(addr(ns, key, j + (lane >> 4), true), b0, b1, b2, b3);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float (&acc)[4] = cur.acc[j + x];
+              float d[4] = {acc[0], acc[1], acc[2], acc[3]};
+              mma_bf16_16816(d, pa, x ? b2 : b0, x ? b3 : b1);
+              acc[0] = mine0 ? d[0] : acc[0];
+              acc[1] = mine0 ? d[1] : acc[1];
+              acc[2] = mine1 ? d[2] : acc[2];
+              acc[3] = mine1 ? d[3] : acc[3];
+            }
+          }
+        }
+      }
+      // a step that was left out would have added +0 to the row: -0 becomes +0 (and x + -0 is x)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float z = row_pos[h] < key0 + 48 ? 0.f : -0.f;
+#pragma unroll
+        for (int j = 0; j < HD / 8; ++j) {
+          cur.acc[j][h * 2] = __fadd_rn(cur.acc[j][h * 2], z);
+          cur.acc[j][h * 2 + 1] = __fadd_rn(cur.acc[j][h * 2 + 1], z);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!row_valid[h] || row_pos[h] < lb) continue;
+      const int64_t at = ((sq.row0 + row_node[h]) * a.Hq + row_head[h]) * a.ntail + t;
+      float* po = a.tail_o + at * HD;
 #pragma unroll
       for (int j = 0; j < HD / 8; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mine[(4 + j * 4 + c) * 32] = cur.acc[j][c];
+        *reinterpret_cast<float2*>(po + j * 8 + tq * 2) = make_float2(cur.acc[j][h * 2], cur.acc[j][h * 2 + 1]);
+      if (tq == 0) *reinterpret_cast<float2*>(a.tail_ml + at * 2) = make_float2(cur.m[h], cur.l[h]);
     }
-    __syncthreads();
-    if (lw == 0 && *abort_flag == 0) {
-      for (int w = 0; w < min(lanes, LANES); ++w) {
-        const float* o = reinterpret_cast<const float*>(smem) + (w * ROWS + rw) * NF * 32 + lane;
-        cur.m[0] = o[0];
-        cur.m[1] = o[32];
-        cur.l[0] = o[64];
-        cur.l[1] = o[96];
+    clear(cur);
+    lb = le;
+  }
+  __syncthreads();
+  if (*abort_flag && tid == 0)  // the copies this CTA started land before it ends
+    for (int i = 0; i < NS; ++i)
+      if (issued[i] >= 0) mbar_wait(&full[i], (issued[i] / NS) & 1);
+}
+
+// ------------------------------------------------------------------------ the lanes before E
+// A CTA owns (sequence, tile of 128 rows, kv head) and up to per_cta splits.  S = Q K^T (K = hd in 16-wide steps,
+// ascending) and O = P V (64 keys in 16-wide steps, ascending) accumulate in TMEM; tcgen05.mma and mma.sync give
+// the same fp32 bits for the same 16-wide steps.  A softmax thread holds one row: its 64 scores of a tile, and the
+// split's running state in registers.  P goes back to TMEM, over the scores it came from, as the A operand of P V.
+// The sums that a quad of mma.sync threads would form are formed by the one thread in the same order: s_q over the
+// keys 8j + 2q + {0, 1}, then (s0 + s1) + (s2 + s3).  Products and sums go two at a time (f32x2: the same
+// roundings).  S of a tile is computed while the one before it is in the softmax, and the accumulator of a finished
+// lane is folded while the next lane's first scores are.
+// Two CTAs share an SM (their chains softmax -> P V -> fold interleave): 114 KB of shared memory and 256 TMEM
+// columns each, and 128 registers a thread at launch, which the warpgroups then split 232 to 24.
+template <int HD>
+struct CtxLayout {
+  static constexpr int kQ = 128 * HD * 2;       // HD/64 boxes of 128 rows x 128 bytes
+  static constexpr int kPage = kKeys * HD * 2;  // one K or V page
+  static constexpr int kSlots = HD == 128 ? 5 : 11;
+  static constexpr int kOffKV = kQ;
+  static constexpr int kOffBar = kOffKV + kSlots * kPage;
+  static constexpr int kBytes = kOffBar + 512;
+  static constexpr int kThreads = 256;
+  static constexpr int kSoftmaxRegs = 232, kOtherRegs = 24, kLaunchRegs = 128;
+  static_assert(128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
+  static constexpr uint32_t kCols = 256, kColS = 0, kColO = 128;  // S0, S1 (64 each; P over them), O (HD)
+};
+
+// D(tmem) (+)= A(tmem) * B(smem desc)^T: A holds two bf16 values of K in each 32-bit column.
+BI_DEV void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Two products, each rounded once: x y + nz with nz = (-0, -0), a value that the compiler cannot see.  (It contracts
+// mul.rn.f32x2 and a following add.rn.f32x2 into one rounding.)
+BI_DEV float2 mul2(float2 x, float2 y, float nz) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %6};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(nz));
+  return r;
+}
+BI_DEV float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 c, a, b;\n"
+      " mov.b64 {%0, %1}, c;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
+    tree_context_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk,
+                        const __grid_constant__ CUtensorMap tmv) {
+  using Lay = CtxLayout<HD>;
+  constexpr int NS = Lay::kSlots;
+  constexpr int kWarpTma = 4, kWarpMma = 5;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + Lay::kOffKV;  // tile i of K0, V0, K1, V1, ... in slot i % NS
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + Lay::kOffBar);
+  uint64_t* kv_empty = kv_full + NS;
+  uint64_t* s_full = kv_empty + NS;  // [2] MMA -> softmax: S of a tile is in TMEM
+  uint64_t* p_full = s_full + 2;     // softmax -> MMA: P written, O folded or rescaled (4 warp arrivals)
+  uint64_t* o_done = p_full + 1;     // MMA -> softmax, MMA: P V of a tile has completed
+  uint64_t* q_full = o_done + 1;     // softmax -> MMA: Q tile loaded (128 thread arrivals)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.y;
+  const int kvh = blockIdx.z % a.Hkv;
+  const int s0 = (blockIdx.z / a.Hkv) * a.per_cta;  // first split of this CTA
+  // The launch before this one (tree_tail_kernel) starts it only after its own predecessors have completed, so q, the
+  // caches and the tables may be read at once (through L2, where those wrote them); what ends below waits for it.
+  const TreeSeq sq = tree_seq(a, b);
+  const int64_t r_first = (int64_t)blockIdx.x * 128;
+  const int64_t n_rows = sq.ok ? (int64_t)sq.n * a.group : 0;
+  int n_tiles = 0;
+  const int ntf = a.split / kKeys;  // tiles of a whole split; tile k is tile k % ntf of split s0 + k / ntf
+  if (r_first < n_rows) {
+    const int E = tail_lane(a, sq.start);
+    const int last = min(s0 + a.per_cta, a.nsplit) * a.split;  // exclusive
+    n_tiles = max(0, min(E, last) - s0 * a.split) / kKeys;
+  }
+  if (n_tiles == 0) {
+    pdl_wait();
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    mbar_init(p_full, 4);
+    mbar_init(o_done, 1);
+    mbar_init(q_full, 128);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(tmem_slot, Lay::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();
+  const int tpl = a.lane_len / kKeys;  // tiles of a lane
+
+  if (warp >= 4) {
+    reg_alloc_dec<Lay::kOtherRegs>();
+    if (warp == kWarpTma && lane == 0) {
+      // ---------------- TMA producer: K and V pages in order
+      const int rows_total = (int)(a.n_blocks * a.Hkv * kKeys);
+      const int32_t* bt = a.block_table + (int64_t)b * a.max_blk;
+      const int page0 = s0 * ntf;
+      int i = 0;
+      int32_t blk = page0 < a.max_blk ? __ldcg(bt + page0) : -1;
+      for (int t = 0; t < n_tiles && !*abort_flag; ++t) {
+        int row = rows_total;  // past the end: the copy reads zeros
+        if (blk >= 0 && blk < a.n_blocks) row = (int)(((int64_t)blk * a.Hkv + kvh) * kKeys);
+        else report(a.status, DEV_BAD_INDEX);
+        if (t + 1 < n_tiles) blk = page0 + t + 1 < a.max_blk ? __ldcg(bt + page0 + t + 1) : -1;
+        for (int v = 0; v < 2 && !*abort_flag; ++v) {
+          const int slot = i % NS;
+          if (i >= NS && !mbar_wait(&kv_empty[slot], ((i / NS) - 1) & 1)) {
+            report(a.status, DEV_TIMEOUT);
+            *abort_flag = 1;
+            break;
+          }
+          uint8_t* dst = sKV + slot * Lay::kPage;
+          mbar_arrive_expect_tx(&kv_full[slot], Lay::kPage);
 #pragma unroll
-        for (int j = 0; j < HD / 8; ++j)
+          for (int x = 0; x < HD / 64; ++x)
+            tma_load_2d(dst + x * (kKeys * 128), v ? &tmv : &tmk, &kv_full[slot], x * 64, row);
+          ++i;
+        }
+      }
+      // the copies this CTA started land before it can exit
+      for (int k = 0; k < NS && k < i; ++k) mbar_wait(&kv_full[(i - 1 - k) % NS], ((i - 1 - k) / NS) & 1);
+    } else if (warp == kWarpMma && lane == 0) {
+      // ---------------- MMA issuer
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, kKeys);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(128, HD) | (1u << 16);  // V read MN-major
+      bool ok = mbar_wait(q_full, 0);
+      auto issue_s = [&](int t) -> bool {
+        const int i = 2 * t;
+        if (!mbar_wait(&kv_full[i % NS], (i / NS) & 1)) return false;
+        tc_fence_after();
+        const uint32_t qa = smem_u32(sQ), ka = smem_u32(sKV + i % NS * Lay::kPage);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) cur.acc[j][c] = o[(4 + j * 4 + c) * 32];
-        lane_merge<HD>(run, cur.m, cur.l, cur.acc);
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32, koff = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
+          tc_mma_bf16(tmem + Lay::kColS + (t & 1) * kKeys, sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + koff),
+                      idesc_s, k != 0 ? 1u : 0u);
+        }
+        tc_commit(&s_full[t & 1]);
+        tc_commit(&kv_empty[i % NS]);
+        return true;
+      };
+      if (ok) ok = issue_s(0);
+      for (int t = 0; ok && t < n_tiles && !*abort_flag; ++t) {
+        // S of tile t + 1 takes the columns that hold P of tile t - 1
+        if (t + 1 < n_tiles && ((t > 0 && !mbar_wait(o_done, (t - 1) & 1)) || !issue_s(t + 1))) {
+          ok = false;
+          break;
+        }
+        const int i = 2 * t + 1;
+        if (!mbar_wait(p_full, t & 1) || !mbar_wait(&kv_full[i % NS], (i / NS) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t va = smem_u32(sKV + i % NS * Lay::kPage);
+        const bool fresh = t % ntf % tpl == 0;  // a lane's first tile starts from nothing
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          tc_mma_bf16_ts(tmem + Lay::kColO, tmem + Lay::kColS + (t & 1) * kKeys + k * 8,
+                         sw128_mnmajor_desc(va + k * 16 * 128, kKeys * 128, 1024), idesc_o,
+                         k == 0 && fresh ? 0u : 1u);
+        tc_commit(o_done);
+        tc_commit(&kv_empty[i % NS]);
+      }
+      if (!ok) {
+        report(a.status, DEV_TIMEOUT);
+        *abort_flag = 1;
       }
     }
   } else {
-    __syncthreads();
-  }
-  if (*abort_flag) {
-    // the copies this CTA started land before it ends
-    if (tid == 0)
-      for (int i = 0; i < NS; ++i)
-        if (issued[i] >= 0) mbar_wait(&full[i], (issued[i] / NS) & 1);
-    return;
-  }
-  if (lw != 0) return;
+    reg_alloc_inc<Lay::kSoftmaxRegs>();
+    // ---------------- softmax: thread tid holds row tid of the tile (its TMEM lane)
+    for (int i = tid; i < 128 * (HD / 8); i += 128) {
+      const int qrow = i / (HD / 8), ch = i % (HD / 8);
+      const int64_t r = r_first + qrow;
+      const bool valid = r < n_rows;
+      const __nv_bfloat16* src =
+          a.q + ((sq.row0 + r / a.group) * a.Hq + kvh * a.group + r % a.group) * HD + ch * 8;
+      cp_async16(sQ + (ch >> 3) * (128 * 128) + qrow * 128 + (((ch & 7) ^ (qrow & 7)) << 4), valid ? src : a.q, valid);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    fence_proxy_async();
+    mbar_arrive(q_full);
+
+    const int64_t r = r_first + tid;
+    const bool valid = r < n_rows;
+    const bool live = r_first + warp * 32 < n_rows;  // the warp has rows
+    const int64_t rec0 = valid ? ((sq.row0 + r / a.group) * a.Hq + kvh * a.group + r % a.group) * a.nsplit : 0;
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const uint32_t tO = tmem + lane_base + Lay::kColO;
+    const float nz = a.neg_zero;
+    float run[HD], run_m = -INFINITY, run_l = 0.f;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (!row_valid[h] || (tail && row_pos[h] < kv_begin)) continue;
-    const int64_t at = ((sq.row0 + row_node[h]) * a.Hq + row_head[h]) * a.nsplit + s;
-    float* po = a.part_o + at * HD;
+    for (int c = 0; c < HD; ++c) run[c] = 0.f;
+    float m = -INFINITY, l = 0.f;  // the lane in progress
+
+    // run <- run (+) (lm, ll, O): lane_merge's formula, an empty run taking O as it is (0 * 0 + O * 1).  The last lane
+    // of a split: the result is split s's record, and run starts over (s < 0: none).
+    auto fold = [&](float lm, float ll, int s) {
+      const float M = fmaxf(run_m, lm);
+      const bool skip = lm == -INFINITY;  // an empty lane leaves the state as it is
+      float fa = run_m == M ? 1.0f : exp2f(__fsub_rn(run_m, M));
+      float fb = lm == M ? 1.0f : exp2f(__fsub_rn(lm, M));
+      if (run_m == -INFINITY) fa = 0.f, fb = 1.f;
+      if (skip) {
+        fa = 1.f;
+        fb = 0.f;
+      } else {
+        run_l = run_m == -INFINITY ? ll : __fadd_rn(__fmul_rn(run_l, fa), __fmul_rn(ll, fb));
+        run_m = M;
+      }
+      const bool any_skip = __any_sync(0xffffffffu, skip);
+      const float2 fa2 = make_float2(fa, fa), fb2 = make_float2(fb, fb);
 #pragma unroll
-    for (int j = 0; j < HD / 8; ++j)
-      *reinterpret_cast<float2*>(po + j * 8 + tq * 2) = make_float2(run.acc[j][h * 2], run.acc[j][h * 2 + 1]);
-    if (tq == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(run.m[h], run.l[h]);
+      for (int c = 0; c < HD; c += 32) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(tO + c, o);
+        tmem_ld_wait();
+        if (any_skip) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = skip ? 0u : o[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          const float2 z = add2(mul2(make_float2(run[c + k], run[c + k + 1]), fa2, nz),
+                                mul2(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), fb2, nz));
+          run[c + k] = z.x;
+          run[c + k + 1] = z.y;
+        }
+        if (s >= 0) {
+          float4* po = reinterpret_cast<float4*>(a.part_o + (rec0 + s) * HD + c);
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            if (valid) po[k / 4] = make_float4(run[c + k], run[c + k + 1], run[c + k + 2], run[c + k + 3]);
+            run[c + k] = run[c + k + 1] = run[c + k + 2] = run[c + k + 3] = 0.f;
+          }
+        }
+      }
+      if (s >= 0) {
+        if (valid) *reinterpret_cast<float2*>(a.part_ml + (rec0 + s) * 2) = make_float2(run_m, run_l);
+        run_m = -INFINITY;
+        run_l = 0.f;
+      }
+    };
+    bool ok = true;
+    int i_split = 0, i_lane = 0;  // tile t is tile i_split of its split, i_lane of its lane
+    for (int t = 0; t < n_tiles; ++t) {
+      ok = mbar_wait(&s_full[t & 1], (t >> 1) & 1);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const bool fresh = i_lane == 0;
+      float alpha = 1.f;
+      const float lm = m, ll = l;  // of the lane before, when this tile starts one
+      if (live) {
+        const uint32_t tS = tmem + lane_base + Lay::kColS + (t & 1) * kKeys;
+        uint32_t s[64];
+        tmem_ld_32x32b_x32(tS, *reinterpret_cast<uint32_t (*)[32]>(&s[0]));
+        tmem_ld_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t (*)[32]>(&s[32]));
+        tmem_ld_wait();
+        // the largest score is the largest product's (scale > 0 and rounding is monotone)
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 64; k += 2)
+          mx[(k >> 1) & 3] = fmaxf(mx[(k >> 1) & 3], fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
+        const float top = __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.scale_log2);
+        const float m_old = fresh ? -INFINITY : m;
+        const float m_new = fmaxf(m_old, top);
+        alpha = m_new == m_old ? 1.0f : exp2f(__fsub_rn(m_old, m_new));
+        const float2 sc = make_float2(a.scale_log2, a.scale_log2);
+        // a row without any key above -inf so far: 2^(-inf - 0) = 0
+        const float neg = m_new == -INFINITY ? 0.f : -m_new;
+        const float2 ng = make_float2(neg, neg);
+        float2 s01 = make_float2(0.f, 0.f), s23 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int h = 0; h < 64; h += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            float p[8];
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+              const float2 x = add2(
+                  mul2(make_float2(__uint_as_float(s[h + j + k]), __uint_as_float(s[h + j + k + 1])), sc, nz), ng);
+              p[k] = exp2_p(x.x);
+              p[k + 1] = exp2_p(x.y);
+              pk[(j + k) / 2] = pack_bf16x2(p[k], p[k + 1]);
+            }
+            s01 = add2(add2(s01, make_float2(p[0], p[2])), make_float2(p[1], p[3]));
+            s23 = add2(add2(s23, make_float2(p[4], p[6])), make_float2(p[5], p[7]));
+          }
+          tmem_st_32x32b_x16(tS + h / 2, pk);
+        }
+        const float rs = __fadd_rn(__fadd_rn(s01.x, s01.y), __fadd_rn(s23.x, s23.y));
+        l = __fadd_rn(__fmul_rn(fresh ? 0.f : l, alpha), rs);
+        m = m_new;
+      }
+      if (t > 0) {
+        ok = mbar_wait(o_done, (t - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        if (live && fresh) {
+          fold(lm, ll, i_split == 0 ? s0 + (t - 1) / ntf : -1);
+        } else if (live && __any_sync(0xffffffffu, alpha != 1.0f)) {
+          const float2 al = make_float2(alpha, alpha);
+#pragma unroll
+          for (int c = 0; c < HD; c += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(tO + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const float2 x = mul2(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), al, nz);
+              o[k] = __float_as_uint(x.x);
+              o[k + 1] = __float_as_uint(x.y);
+            }
+            tmem_st_32x32b_x32(tO + c, o);
+          }
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+      if (++i_lane == tpl) i_lane = 0;
+      if (++i_split == ntf) i_split = i_lane = 0;
+    }
+    if (ok && __all_sync(0xffffffffu, ok)) ok = mbar_wait(o_done, (n_tiles - 1) & 1);
+    if (__all_sync(0xffffffffu, ok)) {
+      tc_fence_after();
+      if (live) fold(m, l, s0 + (n_tiles - 1) / ntf);
+    } else {
+      if (lane == 0) report(a.status, DEV_TIMEOUT);
+      *abort_flag = 1;
+    }
+    tc_fence_before();
   }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, Lay::kCols);
+  pdl_wait();
 }
 
-// The split partials of a row, merged as the attention merge does: one CTA a node, a thread an element.
-__global__ void __launch_bounds__(128) tree_merge_kernel(const TreeArgs a, int hd) {
+// ------------------------------------------------------------------------ the merge
+// A warp a (node, q head), HD / 32 elements a lane.  The splits before E are merged as the attention merge does
+// (weights by lane, sums in ascending order); the split that E cuts and those behind it are first folded from their
+// lanes with lane_merge's formula.
+constexpr int kTreeMergeWarps = 4;
+
+template <int HD>
+__global__ void __launch_bounds__(kTreeMergeWarps * 32) tree_merge_kernel(const TreeArgs a) {
   pdl_trigger();
   pdl_wait();
+  constexpr int NE = HD / 32;
+  const int lane = threadIdx.x & 31;
   const int b = blockIdx.y, i = blockIdx.x;
+  const int head = blockIdx.z * kTreeMergeWarps + (threadIdx.x >> 5);
+  if (head >= a.Hq) return;
   const TreeSeq sq = tree_seq(a, b);
   if (i >= sq.n) return;
   const int64_t row = sq.row0 + i;
-  const int pos = a.row_pos[row];
-  for (int e = blockIdx.z * 128 + threadIdx.x; e < a.Hq * hd; e += gridDim.z * 128) {
-    float v = 0.f;
-    if (pos >= 0)
-      v = merge_split_element(a.part_o, a.part_ml, (row * a.Hq + e / hd) * a.nsplit, pos / a.split + 1, hd, e % hd);
-    a.out[row * a.Hq * hd + e] = f2bf(v);
+  const int pos = __ldcg(a.row_pos + row);
+  __nv_bfloat16* dst = a.out + (row * a.Hq + head) * HD + lane * NE;
+  struct Vec {
+    float v[NE];
+  };
+  auto load = [&](const float* p) {
+    Vec r;
+    if constexpr (NE == 4) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(p + lane * 4));
+      r.v[0] = x.x, r.v[1] = x.y, r.v[2] = x.z, r.v[3] = x.w;
+    } else {
+      const float2 x = __ldcg(reinterpret_cast<const float2*>(p + lane * 2));
+      r.v[0] = x.x, r.v[1] = x.y;
+    }
+    return r;
+  };
+  auto store = [&](const Vec& r) {
+    uint32_t w[NE / 2];
+#pragma unroll
+    for (int e = 0; e < NE; e += 2) w[e / 2] = pack_bf16x2(r.v[e], r.v[e + 1]);
+    if constexpr (NE == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = w[0];
+  };
+  Vec O = {};
+  if (pos < 0) {
+    store(O);
+    return;
   }
+  const int E = tail_lane(a, sq.start);
+  const int sE = sq.start / a.split;           // the split that E stands in
+  const bool cut = E > sE * a.split;           // with lanes before E in it
+  const int64_t rec = row * a.Hq + head;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + rec * a.nsplit;
+  const float2* tml = reinterpret_cast<const float2*>(a.tail_ml) + rec * a.ntail;
+  const float* po = a.part_o + rec * a.nsplit * HD;
+  const float* to = a.tail_o + rec * a.ntail * HD;
+  const int n_ctx = sE + (cut ? 1 : 0);        // records before E
+  // the largest score
+  float M = -INFINITY;
+  for (int s = lane; s < n_ctx; s += 32) M = fmaxf(M, __ldcg(ml + s).x);
+  int n_tail = 0;
+  for (int lb = E; lb <= pos && n_tail < a.ntail; lb = lane_end(a, lb)) {
+    if (lane == 0) M = fmaxf(M, __ldcg(tml + n_tail).x);
+    ++n_tail;
+  }
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.f;
+  for (int c0 = 0; c0 < sE; c0 += 32) {
+    float2 r = make_float2(-INFINITY, 0.f);
+    if (c0 + lane < sE) r = __ldcg(ml + c0 + lane);
+    const float w = merge_weight(r.x, M);
+    for (int k0 = 0; k0 < 32 && c0 + k0 < sE; k0 += 8) {
+      Vec v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c0 + k0 + k < sE) v[k] = load(po + (int64_t)(c0 + k0 + k) * HD);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k0 + k), lk = __shfl_sync(0xffffffffu, r.y, k0 + k);
+        if (c0 + k0 + k < sE) {
+          L = merge_term(L, lk, wk);
+#pragma unroll
+          for (int e = 0; e < NE; ++e) O.v[e] = merge_term(O.v[e], v[k].v[e], wk);
+        }
+      }
+    }
+  }
+  // the split that E cuts, and those behind it
+  Vec P = {};
+  float pm = -INFINITY, pl = 0.f;
+  if (cut) {
+    const float2 r = __ldcg(ml + sE);
+    pm = r.x;
+    pl = r.y;
+    P = load(po + (int64_t)sE * HD);
+  }
+  int t = 0;
+  for (int lb = E; t < n_tail; ++t) {
+    const float2 r = __ldcg(tml + t);
+    const Vec Q = load(to + (int64_t)t * HD);
+    if (r.x != -INFINITY) {
+      if (pm == -INFINITY) {
+        pm = r.x;
+        pl = r.y;
+        P = Q;
+      } else {
+        const float m = fmaxf(pm, r.x);
+        const float fa = pm == m ? 1.0f : exp2f(__fsub_rn(pm, m));
+        const float fb = r.x == m ? 1.0f : exp2f(__fsub_rn(r.x, m));
+        pl = __fadd_rn(__fmul_rn(pl, fa), __fmul_rn(r.y, fb));
+#pragma unroll
+        for (int e = 0; e < NE; ++e) P.v[e] = __fadd_rn(__fmul_rn(P.v[e], fa), __fmul_rn(Q.v[e], fb));
+        pm = m;
+      }
+    }
+    const int le = lane_end(a, lb);
+    if (le % a.split == 0 || t + 1 == n_tail) {  // the split ends, or the row does
+      const float w = merge_weight(pm, M);
+      L = merge_term(L, pl, w);
+#pragma unroll
+      for (int e = 0; e < NE; ++e) O.v[e] = merge_term(O.v[e], P.v[e], w);
+      P = {};
+      pm = -INFINITY;
+      pl = 0.f;
+    }
+    lb = le;
+  }
+#pragma unroll
+  for (int e = 0; e < NE; ++e) O.v[e] = __fdiv_rn(O.v[e], L);
+  store(O);
 }
 
-template <int HD, int ROWS, int LANES>
-static bi_status launch_tree(TreeArgs args, int64_t B, int want_stages, int min_stages, const CUtensorMap& tmk,
-                             const CUtensorMap& tmv, cudaStream_t st) {
-  using Lay = TreeLayout<HD, ROWS * LANES>;
+// Records of a row's lanes from E on: its positions there are at most `max_nodes` from anywhere in a lane.
+static int tail_records(int64_t max_nodes, int split, int lane_len) {
+  const int shortest = split % lane_len ? split % lane_len : lane_len;
+  return (int)((max_nodes - 1 + lane_len - 1) / shortest) + 1;
+}
+static int split_lane_len(int split) { return ((split + 3) / 4 + kKeys - 1) / kKeys * kKeys; }
+
+template <int HD>
+static bi_status launch_tree(TreeArgs args, int64_t B, cudaStream_t st) {
+  using Tail = TailLayout<HD>;
+  using Ctx = CtxLayout<HD>;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
+  static int ctx_regs = 0;
   constexpr int kMost = 227 * 1024;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(tree_attention_kernel<HD, ROWS, LANES>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    attr_err = cudaFuncSetAttribute(tree_tail_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (attr_err == cudaSuccess)
+      attr_err = cudaFuncSetAttribute(tree_context_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ctx::kBytes);
+    cudaFuncAttributes fa{};
+    if (attr_err == cudaSuccess) attr_err = cudaFuncGetAttributes(&fa, tree_context_kernel<HD>);
+    ctx_regs = fa.numRegs;
   });
   if (attr_err != cudaSuccess)
-    return fail(BI_ERR_CUDA, std::string("tree attention smem attribute: ") + cudaGetErrorString(attr_err));
-  args.stages = std::max(want_stages, min_stages);
-  const int smem = Lay::bytes(args.stages, args.split);
-  if (args.stages > Lay::kMaxStages || smem > kMost)
-    return fail(BI_ERR_UNSUPPORTED_SHAPE, "bi_tree_attention: the tree does not fit shared memory");
-  const dim3 grid((unsigned)cdiv((int64_t)args.max_nodes * args.group, ROWS * 16), (unsigned)B,
-                  (unsigned)(args.Hkv * args.nsplit));
-  return launched(launch_pdl(tree_attention_kernel<HD, ROWS, LANES>, grid, dim3(ROWS * LANES * 32), smem, st, args,
-                             tmk, tmv),
-                  "tree_attention_kernel");
+    return fail(BI_ERR_CUDA, std::string("tree attention attributes: ") + cudaGetErrorString(attr_err));
+  // the warpgroups' register split must fit what the block launches with, or the increase would never be granted
+  if (ctx_regs < Ctx::kLaunchRegs)
+    return fail(BI_ERR_CUDA, "tree attention: compiled with fewer registers than its warpgroup split needs");
+  CUtensorMap tmk, tmv;
+  const uint64_t rows = (uint64_t)args.n_blocks * args.Hkv * kKeys;
+  if (!encode_tmap_2d_bf16(&tmk, args.k_cache, HD, rows, HD * 2, 64, kKeys, true) ||
+      !encode_tmap_2d_bf16(&tmv, args.v_cache, HD, rows, HD * 2, 64, kKeys, true))
+    return fail(BI_ERR_CUDA, "bi_tree_attention: cuTensorMapEncodeTiled failed for the K/V cache");
+  // pages that can hold a tile's nodes and their ancestors together with the last context tokens before them
+  args.stages = std::max(HD == 128 ? 3 : 6, (63 + args.max_nodes + 63) / 64);
+  const int64_t r = (int64_t)args.max_nodes * args.group;
+  BI_TRY(launched(launch_pdl(tree_tail_kernel<HD>,
+                             dim3((unsigned)cdiv(r, kTailWarps * 16), (unsigned)B, (unsigned)args.Hkv),
+                             dim3(kTailWarps * 32), Tail::bytes(args.stages), st, args, tmk, tmv),
+                  "tree_tail_kernel"));
+  args.per_cta = 1;
+  BI_TRY(launched(launch_pdl(tree_context_kernel<HD>,
+                             dim3((unsigned)cdiv(r, 128), (unsigned)B,
+                                  (unsigned)(args.Hkv * cdiv(args.nsplit, args.per_cta))),
+                             dim3(Ctx::kThreads), Ctx::kBytes, st, args, tmk, tmv),
+                  "tree_context_kernel"));
+  return launched(launch_pdl(tree_merge_kernel<HD>,
+                             dim3((unsigned)args.max_nodes, (unsigned)B, (unsigned)cdiv(args.Hq, kTreeMergeWarps)),
+                             dim3(kTreeMergeWarps * 32), 0, st, args),
+                  "tree_merge_kernel");
 }
 
 }  // namespace bi
@@ -537,8 +991,9 @@ extern "C" {
 
 size_t bi_tree_attention_workspace_size(int64_t max_T, int Hq, int hd, int64_t max_ctx, int kv_split) {
   if (max_T <= 0 || Hq <= 0 || hd <= 0 || max_ctx <= 0 || kv_split < 64) return 0;
-  const size_t per = (size_t)max_T * Hq * bi::cdiv(max_ctx, kv_split);
-  return per * (hd + 2) * sizeof(float) + (size_t)max_T * sizeof(int32_t) + 256;
+  const size_t recs = bi::cdiv(max_ctx, kv_split) +
+                      bi::tail_records(bi::kMaxTreeNodes, kv_split, bi::split_lane_len(kv_split));
+  return (size_t)max_T * Hq * recs * (hd + 2) * sizeof(float) + (size_t)max_T * sizeof(int32_t) + 256;
 }
 
 bi_status bi_tree_attention(const void* q, int64_t T, const int32_t* parent, const int32_t* row0, const int32_t* start,
@@ -558,6 +1013,7 @@ bi_status bi_tree_attention(const void* q, int64_t T, const int32_t* parent, con
   BI_REQUIRE_SHAPE(64 % group == 0, "64 must be a multiple of Hq/Hkv");
   BI_REQUIRE(kv_split >= 64 && kv_split % 64 == 0, "kv_split must be a positive multiple of 64");
   BI_REQUIRE_SHAPE(kv_split <= kTreeMaxSplit, "kv_split must be at most 16384");
+  BI_REQUIRE(scale > 0, "scale must be positive");
   BI_REQUIRE(max_ctx > 0 && max_blocks_per_seq > 0 && n_blocks > 0, "bad max_ctx or cache shape");
   BI_REQUIRE_SHAPE(n_blocks < (int64_t(1) << 31) / 64 / Hkv && max_blocks_per_seq <= 0x7fffffff / 64 &&
                        max_ctx <= 0x7fffffff - 2 * kTreeMaxSplit,
@@ -566,8 +1022,10 @@ bi_status bi_tree_attention(const void* q, int64_t T, const int32_t* parent, con
              "pointers must be 16-byte aligned");
   const int64_t ns = cdiv(max_ctx, kv_split);
   BI_REQUIRE(B <= 65535 && Hkv * ns <= 65535 && T <= 0x7fffffff, "too many sequences, rows or splits");
-  const size_t per = (size_t)T * Hq * ns;
-  BI_REQUIRE(ws_bytes >= per * (hd + 2) * sizeof(float) + (size_t)T * sizeof(int32_t),
+  const int lane_len = split_lane_len(kv_split);
+  const int nt = tail_records(max_nodes, kv_split, lane_len);
+  const size_t per = (size_t)T * Hq * ns, per_t = (size_t)T * Hq * nt;
+  BI_REQUIRE(ws_bytes >= (per + per_t) * (hd + 2) * sizeof(float) + (size_t)T * sizeof(int32_t),
              "workspace too small (bi_tree_attention_workspace_size)");
   TreeArgs a;
   a.q = static_cast<const __nv_bfloat16*>(q);
@@ -576,8 +1034,12 @@ bi_status bi_tree_attention(const void* q, int64_t T, const int32_t* parent, con
   a.start = start;
   a.block_table = block_table;
   a.part_o = static_cast<float*>(workspace);
-  a.part_ml = a.part_o + per * hd;
-  a.row_pos = reinterpret_cast<int32_t*>(a.part_ml + per * 2);
+  a.tail_o = a.part_o + per * hd;
+  a.part_ml = a.tail_o + per_t * hd;
+  a.tail_ml = a.part_ml + per * 2;
+  a.row_pos = reinterpret_cast<int32_t*>(a.tail_ml + per_t * 2);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.status = device_status_ptr();
   a.T = T;
@@ -588,28 +1050,13 @@ bi_status bi_tree_attention(const void* q, int64_t T, const int32_t* parent, con
   a.Hkv = Hkv;
   a.group = group;
   a.nsplit = (int)ns;
+  a.ntail = nt;
+  a.lane_len = lane_len;
   a.split = kv_split;
-  a.stages = 0;
+  a.stages = a.per_cta = 0;
   a.scale_log2 = scale * 1.4426950408889634f;
-  CUtensorMap tmk, tmv;
-  const uint64_t rows = (uint64_t)n_blocks * Hkv * kKeys;
-  if (!encode_tmap_2d_bf16(&tmk, k_cache, hd, rows, hd * 2, 64, kKeys, true) ||
-      !encode_tmap_2d_bf16(&tmv, v_cache, hd, rows, hd * 2, 64, kKeys, true))
-    return fail(BI_ERR_CUDA, "bi_tree_attention: cuTensorMapEncodeTiled failed for the K/V cache");
-  cudaStream_t st = as_stream(stream);
-  // pages that can hold a tree's nodes together with the last context tokens before them
-  const int tail = (int)((63 + max_nodes + 63) / 64);
-  const int64_t r = max_nodes * group;
-  bi_status s;
-  if (r <= 16)
-    s = hd == 64 ? launch_tree<64, 1, 4>(a, B, 6, tail, tmk, tmv, st) : launch_tree<128, 1, 4>(a, B, 6, tail, tmk, tmv, st);
-  else if (r <= 32)
-    s = hd == 64 ? launch_tree<64, 2, 4>(a, B, 6, tail, tmk, tmv, st) : launch_tree<128, 2, 4>(a, B, 6, tail, tmk, tmv, st);
-  else
-    s = hd == 64 ? launch_tree<64, 4, 1>(a, B, 6, tail, tmk, tmv, st) : launch_tree<128, 4, 1>(a, B, 3, tail, tmk, tmv, st);
-  BI_TRY(s);
-  const dim3 mgrid((unsigned)max_nodes, (unsigned)B, (unsigned)std::min<int64_t>(cdiv(Hq * hd, 128), 65535));
-  return launched(launch_pdl(tree_merge_kernel, mgrid, dim3(128), 0, st, a, hd), "tree_merge_kernel");
+  a.neg_zero = -0.f;
+  return hd == 64 ? launch_tree<64>(a, B, as_stream(stream)) : launch_tree<128>(a, B, as_stream(stream));
 }
 
 }  // extern "C"
