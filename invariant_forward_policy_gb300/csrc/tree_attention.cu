@@ -131,19 +131,52 @@ __device__ __forceinline__ void tree_softmax(float (&sc)[8][4], int key0, const 
   }
 }
 
-// acc += P V of one 64-key tile: four 16-key steps in order, P rounded to bf16.
-template <int HD>
-__device__ __forceinline__ void tree_pv(uint32_t sv, const float (&p)[8][4], int lane, LaneState<HD>& st) {
+// Shared-memory address of 16-byte chunk ch of a key row that begins at `row` (rows of 128 bytes under the 128-byte
+// swizzle; the second 64 head dims 8 KB on).
+BI_DEV uint32_t row_chunk(uint32_t row, int ch) {
+  return row + (ch >> 3) * (kKeys * 128) + ((((uint32_t)ch & 7) ^ ((row >> 7) & 7)) << 4);
+}
+
+// S = Q K^T of the first `groups` 8-key groups of a tile (0 for the others), in 16-wide steps of hd, the groups'
+// chains side by side.  row(key): the address of the key's row.
+template <int HD, typename Row>
+__device__ __forceinline__ void tree_scores(const uint32_t (&qf)[HD / 16][4], int lane, float (&sc)[8][4], Row row,
+                                            int groups) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+#pragma unroll
+  for (int j0 = 0; j0 < 8; j0 += 4) {
+    if (j0 >= groups) break;
+    uint32_t r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = row((j0 + j) * 8 + (lane & 7));
+#pragma unroll
+    for (int kk = 0; kk < HD / 16; kk += 2) {
+      uint32_t k[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ldsm_x4(row_chunk(r[j], kk * 2 + (lane >> 3)), k[j][0], k[j][1], k[j][2], k[j][3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mma_bf16_16816(sc[j0 + j], qf[kk], k[j][0], k[j][1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mma_bf16_16816(sc[j0 + j], qf[kk + 1], k[j][2], k[j][3]);
+    }
+  }
+}
+
+// acc += P V of the first `steps` 16-key steps of a tile, in order, P rounded to bf16.
+template <int HD, typename Row>
+__device__ __forceinline__ void tree_pv(const float (&p)[8][4], int lane, LaneState<HD>& st, Row row, int steps) {
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) {
+    if (kk >= steps) break;
     const uint32_t pa[4] = {pack_bf16x2(p[2 * kk][0], p[2 * kk][1]), pack_bf16x2(p[2 * kk][2], p[2 * kk][3]),
                             pack_bf16x2(p[2 * kk + 1][0], p[2 * kk + 1][1]),
                             pack_bf16x2(p[2 * kk + 1][2], p[2 * kk + 1][3])};
+    const uint32_t r = row(kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8);
 #pragma unroll
     for (int j = 0; j < HD / 8; j += 2) {
-      const int key = kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
       uint32_t b0, b1, b2, b3;
-      ldsm_x4_t(sv + kv_off<HD>(key, j + (lane >> 4)), b0, b1, b2, b3);
+      ldsm_x4_t(row_chunk(r, j + (lane >> 4)), b0, b1, b2, b3);
       mma_bf16_16816(st.acc[j], pa, b0, b1);
       mma_bf16_16816(st.acc[j + 1], pa, b2, b3);
     }
@@ -151,25 +184,28 @@ __device__ __forceinline__ void tree_pv(uint32_t sv, const float (&p)[8][4], int
 }
 
 // ------------------------------------------------------------------------ the lanes from E on
-// A CTA owns (sequence, tile of 64 rows, kv head).  Pages come by TMA into a ring.  The few pages before position
-// `start` count for every row and are run over by every warp's 16 rows.  Tiles that hold positions from `start` on
-// differ by node: the pages that hold the tree's own keys are then all in the ring at once, and a node's tile is
-// read by ldmatrix with a row address for each position (the page's row for a position before `start`, the path
-// node's row behind it).  An 8-key group of scores or a 16-key step of P V whose positions all stand before `start`
-// is done for the warp's 16 rows at once, the others once for each node of the warp; a row keeps its own node's
-// result, so no other node's key or value reaches it.
-constexpr int kTailWarps = 4;
+// A warp owns a node's q heads of one kv head (a 16-row tile; groups of 32 and 64 heads take two and four warps), a
+// CTA eight neighbouring ones, whose keys and values come by TMA into its shared memory once: the pages of the first
+// lane before position `start`, through a ring, then all pages that hold the tree's own keys at once.  ldmatrix takes
+// an address for every key row, so a tile behind `start` is read as if the node's path stood in the cache: the page's
+// row for a position before `start`, the path node's row behind it, a row of zeros behind the node (as a plain decode
+// reads positions behind its own).  8-key groups of scores and 16-key steps of P V behind the node's position are
+// left out.  Most of a 16-row tile is empty for small groups; the chain of one node's few tiles is the time.
+constexpr int kTailWarps = 8;
 
-// Shared memory: the page ring, then barriers, a row of zeros, depths, parents and the warps' path tables.
+// Shared memory: the page ring; then barriers, depths, parents, the warps' path tables.  The zero row is 128 bytes
+// behind the ring and, for the second half of 128 head dims, 128 bytes 8 KB on: where V would be of a K row kPage
+// before them.
 template <int HD>
 struct TailLayout {
   static constexpr int kPage = kKeys * HD * 2;
   static constexpr int kStage = 2 * kPage;  // a K page and its V page
   static constexpr int kMaxStages = 12;
-  static constexpr int kZero = HD * 2;      // a key row of zeros
-  static int bytes(int stages) {
-    return 1024 + stages * kStage + 256 + kZero + kMaxTreeNodes * 4 + kTailWarps * 16 * kKeys * 2;
-  }
+  static constexpr int kOffBar = 128, kOffDepth = 512, kOffParent = kOffDepth + 2 * kMaxTreeNodes,
+                       kOffPath = kOffParent + 2 * kMaxTreeNodes,
+                       kExtra = HD == 128 ? kKeys * 128 + 128 : kOffPath + kTailWarps * kKeys * 2;
+  static_assert(kOffPath + kTailWarps * kKeys * 2 <= kKeys * 128, "the tables end before the second zero row");
+  static int bytes(int stages) { return 1024 + stages * kStage + kExtra; }
 };
 
 template <int HD>
@@ -181,15 +217,14 @@ __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(const TreeAr
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int NS = a.stages;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + NS * Lay::kStage);  // [NS] the stage's pages have landed
-  uint64_t* empty = full + Lay::kMaxStages;                               // [NS] the warps have read them
+  uint8_t* extra = smem + NS * Lay::kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(extra + Lay::kOffBar);  // [NS] the stage's pages have landed
+  uint64_t* empty = full + Lay::kMaxStages;                            // [NS] the warps have read them
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + Lay::kMaxStages);
-  int* max_depth = const_cast<int*>(abort_flag) + 1;
-  volatile int* issued = abort_flag + 2;  // [NS] the page that was last asked for in each stage
-  uint8_t* zero_row = smem + NS * Lay::kStage + 256;
-  int16_t* depth_of = reinterpret_cast<int16_t*>(zero_row + Lay::kZero);
-  int16_t* parent_of = depth_of + kMaxTreeNodes;
-  uint16_t* paths = reinterpret_cast<uint16_t*>(parent_of + kMaxTreeNodes);  // [WARPS][16][64]
+  volatile int* issued = abort_flag + 1;  // [NS] the page that was last asked for in each stage
+  int16_t* depth_of = reinterpret_cast<int16_t*>(extra + Lay::kOffDepth);
+  int16_t* parent_of = reinterpret_cast<int16_t*>(extra + Lay::kOffParent);
+  uint16_t* paths = reinterpret_cast<uint16_t*>(extra + Lay::kOffPath);  // [WARPS][64]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.y, kvh = blockIdx.z;
   if (tid == 0) {
@@ -201,7 +236,8 @@ __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(const TreeAr
     *abort_flag = 0;
     fence_barrier_init();
   }
-  for (int i = tid; i < Lay::kZero / 4; i += WARPS * 32) reinterpret_cast<uint32_t*>(zero_row)[i] = 0u;
+  if (tid < 32) reinterpret_cast<uint32_t*>(extra)[tid] = 0u;
+  if (HD == 128 && tid >= 32 && tid < 64) reinterpret_cast<uint32_t*>(extra + kKeys * 128)[tid - 32] = 0u;
   // the context kernel reads what this kernel's predecessors wrote without waiting for this one: it may start only
   // once they have completed
   pdl_wait();
@@ -209,11 +245,12 @@ __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(const TreeAr
   const TreeSeq sq = tree_seq(a, b);
   const bool speaks = kvh == 0;  // reports the sequence's faults and writes positions
   const int n = sq.n, start = sq.start;
-  const int64_t r_first = (int64_t)blockIdx.x * WARPS * 16;  // the tile's first row of the sequence's n * group
-  const int node0 = (int)(r_first / a.group);
+  const int parts = (a.group + 15) / 16;  // warps of a node
+  const int per_cta = WARPS / parts;      // nodes of a CTA
+  const int node0 = blockIdx.x * per_cta;
   if (speaks && blockIdx.x == 0 && tid == 0 && !sq.ok) report(a.status, DEV_BAD_INDEX);
   if (node0 >= n) return;
-  const int last_node = min(n, (int)((r_first + WARPS * 16 + a.group - 1) / a.group)) - 1;
+  const int last_node = min(n, node0 + per_cta) - 1;
   if (!sq.ok) {
     if (speaks)
       for (int i = node0 + tid; i <= last_node; i += WARPS * 32) a.row_pos[sq.row0 + i] = -1;
@@ -245,47 +282,40 @@ __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(const TreeAr
     for (int j = 0; j < NS && j < n_issue; ++j) issue(j);
   if (warp == WARPS - 1) {
     const bool bad = tree_depths(a.parent + sq.row0, last_node + 1, depth_of, lane, parent_of);
-    int deep = -1;
     bool far = false;
     for (int i = node0 + lane; i <= last_node; i += 32) {
       const int d = depth_of[i];
       const bool fits = start + d < a.nsplit * a.split;
       far |= !fits;
-      if (d >= 0 && fits) deep = max(deep, d);
       if (speaks) a.row_pos[sq.row0 + i] = d >= 0 && fits ? start + d : -1;
     }
-    for (int o = 16; o; o >>= 1) deep = max(deep, __shfl_xor_sync(0xffffffffu, deep, o));
     far = __any_sync(0xffffffffu, far);
-    if (lane == 0) *max_depth = deep;
     if (speaks && (bad || far)) report(a.status, DEV_BAD_INDEX);
   }
 
-  // this warp's rows: node, q head and position of the two a thread holds
+  // the rows that a thread holds: q heads g and g + 8 of the node's group (or of the warp's 16 of it)
   const int g = lane >> 2, tq = lane & 3;
-  const int64_t wr0 = r_first + warp * 16;
-  int row_node[2], row_pos[2], row_head[2];
-  bool row_valid[2];
+  const int node = node0 + warp / parts;
+  const int h0 = warp % parts * 16;
+  const bool there = node <= last_node && warp < per_cta * parts;
   uint32_t qf[HD / 16][4];
+  int row_head[2];
+  bool row_valid[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int64_t r = wr0 + g + h * 8;
-    row_node[h] = (int)(r / a.group);
-    row_valid[h] = row_node[h] < n;
-    row_head[h] = kvh * a.group + (int)(r % a.group);
-    const __nv_bfloat16* qr = a.q + ((sq.row0 + row_node[h]) * a.Hq + row_head[h]) * HD + tq * 2;
+    row_valid[h] = there && h0 + g + h * 8 < a.group;
+    row_head[h] = kvh * a.group + h0 + g + h * 8;
+    const __nv_bfloat16* qr = a.q + ((sq.row0 + node) * a.Hq + row_head[h]) * HD + tq * 2;
 #pragma unroll
     for (int kk = 0; kk < HD / 16; ++kk) {
-      qf[kk][h] = row_valid[h] ? *reinterpret_cast<const uint32_t*>(qr + kk * 16) : 0u;
-      qf[kk][2 + h] = row_valid[h] ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8) : 0u;
+      qf[kk][h] = row_valid[h] ? __ldcg(reinterpret_cast<const uint32_t*>(qr + kk * 16)) : 0u;
+      qf[kk][2 + h] = row_valid[h] ? __ldcg(reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8)) : 0u;
     }
   }
   __syncthreads();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int d = row_valid[h] ? depth_of[row_node[h]] : -1;
-    row_pos[h] = d >= 0 && start + d < a.nsplit * a.split ? start + d : -1;
-  }
-  const int end = start + *max_depth + 1;  // behind the last position that a row of the tile sees
+  const int d = there ? depth_of[node] : -1;
+  const bool live = d >= 0 && start + d < a.nsplit * a.split;
+  const int pos = start + d;
 
   bool ok = true;
   auto wait_page = [&](int j) {
@@ -295,21 +325,18 @@ __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(const TreeAr
     }
     return (bool)__all_sync(0xffffffffu, *abort_flag == 0);
   };
-  uint16_t* path = paths + warp * 16 * kKeys;
-  const int per_node = min(a.group, 16);           // rows of a node in this warp
-  const int n_slots = 16 / per_node;               // nodes of this warp
-  const int wnode0 = (int)(wr0 / a.group);
-  const int wlast = min(n, wnode0 + n_slots) - 1;  // the warp's last node
-
   LaneState<HD> cur;
   clear(cur);
   for (int j = 0; ok && j < n_plain; ++j) {
     if (!(ok = wait_page(j))) break;
     const uint32_t sk = smem_u32(smem + j % NS * Lay::kStage);
-    float sc[8][4];
-    attn_scores<HD, 2>(sk, qf, lane, sc);
-    tree_softmax<HD, false>(sc, 0, row_pos, a.scale_log2, lane, cur);
-    tree_pv<HD>(sk + Lay::kPage, sc, lane, cur);
+    if (live) {
+      float sc[8][4];
+      tree_scores<HD>(qf, lane, sc, [&](int key) { return sk + key * 128; }, 8);
+      const int all[2] = {0x7fffffff, 0x7fffffff};
+      tree_softmax<HD, false>(sc, 0, all, a.scale_log2, lane, cur);
+      tree_pv<HD>(sc, lane, cur, [&](int key) { return sk + Lay::kPage + key * 128; }, 4);
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[j % NS]);
     if (tid == 0 && j + NS < n_issue) {  // the freed stage takes the page NS places on
@@ -323,103 +350,49 @@ __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(const TreeAr
     __syncwarp();
   }
   for (int i = 0; ok && i < tail_pages; ++i) ok = wait_page(n_plain + i);
+  uint16_t* path = paths + warp * kKeys;
+  const int first_slot = n_plain % NS;
+  const uint32_t base = smem_u32(smem);
+  const uint32_t zero = base + NS * Lay::kStage - Lay::kPage;  // its V is the zero row
   int lb = E;
-  for (int t = 0; ok && t < a.ntail && lb < end; ++t) {
+  for (int t = 0; ok && live && t < a.ntail && lb <= pos; ++t) {
     const int le = lane_end(a, lb);
-    for (int key0 = max(lb, tail0); key0 < min(le, end); key0 += kKeys) {
-      // path[slot][i]: the row, among the tail pages' rows, of position key0 + i (0xffff: none, a row of zeros)
-      __syncwarp();
-      for (int i = lane; i < n_slots * kKeys; i += 32) {
-        const int p = key0 + i % kKeys;
-        path[i] = p < start ? (uint16_t)(p - tail0) : (uint16_t)0xffff;
-      }
-      __syncwarp();
-      int wdeep = -1;  // the deepest of the warp's nodes
-      if (lane < n_slots && wnode0 + lane <= wlast) {
-        int node = wnode0 + lane;
-        wdeep = depth_of[node];
-        for (int p = start + wdeep; p >= start && p >= key0; --p) {
-          if (p < key0 + kKeys) path[lane * kKeys + p - key0] = (uint16_t)(start - tail0 + node);
-          node = parent_of[node];
-        }
-      }
-      for (int o = 8; o; o >>= 1) wdeep = max(wdeep, __shfl_xor_sync(0xffffffffu, wdeep, o));
-      wdeep = __shfl_sync(0xffffffffu, wdeep, 0);
-      __syncwarp();
-      // byte address of chunk ch of position i of node slot ns; v: of the V page
-      auto addr = [&](int ns, int i, int ch, bool v) -> uint32_t {
-        const int off = path[ns * kKeys + i];
-        if (off == 0xffff) return smem_u32(zero_row) + ch * 16;
-        const int pg = n_plain + off / kKeys;
-        return smem_u32(smem + pg % NS * Lay::kStage + (v ? Lay::kPage : 0)) + kv_off<HD>(off % kKeys, ch);
+    for (int key0 = max(lb, tail0); key0 < min(le, pos + 1); key0 += kKeys) {
+      // path[i]: the key row of position key0 + i, in units of 128 bytes of shared memory
+      auto row_of = [&](int off) {  // off: from the first tail page's first row
+        int slot = first_slot + off / kKeys;
+        if (slot >= NS) slot -= NS;
+        return (uint16_t)(slot * (Lay::kStage / 128) + off % kKeys);
       };
+      __syncwarp();
+      for (int i = lane; i < kKeys; i += 32)
+        path[i] = key0 + i < start ? row_of(key0 + i - tail0) : (uint16_t)((zero - base) / 128);
+      __syncwarp();
+      if (lane == 0) {
+        int x = node;
+        for (int p = pos; p >= start && p >= key0; --p) {
+          if (p < key0 + kKeys) path[p - key0] = row_of(start - tail0 + x);
+          x = parent_of[x];
+        }
+      }
+      __syncwarp();
       float sc[8][4];
+      tree_scores<HD>(qf, lane, sc, [&](int key) { return base + path[key] * 128u; }, min(8, (pos - key0) / 8 + 1));
+      const int at[2] = {pos, pos};
+      tree_softmax<HD, true>(sc, key0, at, a.scale_log2, lane, cur);
+      const int steps = min(4, (pos - key0) / 16 + 1);
+      tree_pv<HD>(sc, lane, cur, [&](int key) { return base + Lay::kPage + path[key] * 128u; }, steps);
+      if (steps < 4) {  // a step that is left out would have added +0: -0 becomes +0
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
-        const bool shared = key0 + j * 8 + 7 < start;
-        for (int ns = 0; ns < (shared ? 1 : n_slots); ++ns) {
-          // a node without a position in this group of keys: its scores there are masked
-          if (!shared && (wnode0 + ns > wlast || start + depth_of[wnode0 + ns] < key0 + j * 8)) continue;
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < HD / 8; ++j)
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; kk += 2) {
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4(addr(ns, j * 8 + (lane & 7), kk * 2 + (lane >> 3), false), b0, b1, b2, b3);
-            mma_bf16_16816(d, qf[kk], b0, b1);
-            mma_bf16_16816(d, qf[kk + 1], b2, b3);
-          }
-          const bool mine0 = shared || g / per_node == ns, mine1 = shared || (g + 8) / per_node == ns;
-          sc[j][0] = mine0 ? d[0] : sc[j][0];
-          sc[j][1] = mine0 ? d[1] : sc[j][1];
-          sc[j][2] = mine1 ? d[2] : sc[j][2];
-          sc[j][3] = mine1 ? d[3] : sc[j][3];
-        }
-      }
-      tree_softmax<HD, true>(sc, key0, row_pos, a.scale_log2, lane, cur);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const uint32_t pa[4] = {pack_bf16x2(sc[2 * kk][0], sc[2 * kk][1]), pack_bf16x2(sc[2 * kk][2], sc[2 * kk][3]),
-                                pack_bf16x2(sc[2 * kk + 1][0], sc[2 * kk + 1][1]),
-                                pack_bf16x2(sc[2 * kk + 1][2], sc[2 * kk + 1][3])};
-        const bool shared = key0 + kk * 16 + 15 < start;
-        for (int ns = 0; ns < (shared ? 1 : n_slots); ++ns) {
-          // P is zero for a node without a position in this step
-          if (!shared && (wnode0 + ns > wlast || start + depth_of[wnode0 + ns] < key0 + kk * 16)) continue;
-          const bool mine0 = shared || g / per_node == ns, mine1 = shared || (g + 8) / per_node == ns;
-#pragma unroll
-          for (int j = 0; j < HD / 8; j += 2) {
-            const int key = kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4_t(addr(ns, key, j + (lane >> 4), true), b0, b1, b2, b3);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              float (&acc)[4] = cur.acc[j + x];
-              float d[4] = {acc[0], acc[1], acc[2], acc[3]};
-              mma_bf16_16816(d, pa, x ? b2 : b0, x ? b3 : b1);
-              acc[0] = mine0 ? d[0] : acc[0];
-              acc[1] = mine0 ? d[1] : acc[1];
-              acc[2] = mine1 ? d[2] : acc[2];
-              acc[3] = mine1 ? d[3] : acc[3];
-            }
-          }
-        }
-      }
-      // a step that was left out would have added +0 to the row: -0 becomes +0 (and x + -0 is x)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float z = row_pos[h] < key0 + 48 ? 0.f : -0.f;
-#pragma unroll
-        for (int j = 0; j < HD / 8; ++j) {
-          cur.acc[j][h * 2] = __fadd_rn(cur.acc[j][h * 2], z);
-          cur.acc[j][h * 2 + 1] = __fadd_rn(cur.acc[j][h * 2 + 1], z);
-        }
+          for (int c = 0; c < 4; ++c) cur.acc[j][c] = __fadd_rn(cur.acc[j][c], 0.f);
       }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (!row_valid[h] || row_pos[h] < lb) continue;
-      const int64_t at = ((sq.row0 + row_node[h]) * a.Hq + row_head[h]) * a.ntail + t;
+      if (!row_valid[h]) continue;
+      const int64_t at = ((sq.row0 + node) * a.Hq + row_head[h]) * a.ntail + t;
       float* po = a.tail_o + at * HD;
 #pragma unroll
       for (int j = 0; j < HD / 8; ++j)
@@ -969,8 +942,9 @@ static bi_status launch_tree(TreeArgs args, int64_t B, cudaStream_t st) {
   // pages that can hold a tile's nodes and their ancestors together with the last context tokens before them
   args.stages = std::max(HD == 128 ? 3 : 6, (63 + args.max_nodes + 63) / 64);
   const int64_t r = (int64_t)args.max_nodes * args.group;
+  const int per_cta = kTailWarps / ((args.group + 15) / 16);  // nodes of a CTA
   BI_TRY(launched(launch_pdl(tree_tail_kernel<HD>,
-                             dim3((unsigned)cdiv(r, kTailWarps * 16), (unsigned)B, (unsigned)args.Hkv),
+                             dim3((unsigned)cdiv(args.max_nodes, per_cta), (unsigned)B, (unsigned)args.Hkv),
                              dim3(kTailWarps * 32), Tail::bytes(args.stages), st, args, tmk, tmv),
                   "tree_tail_kernel"));
   args.per_cta = 1;
