@@ -40,7 +40,7 @@ struct TreeArgs {
   __nv_bfloat16* out;
   int* status;
   int64_t T, max_blk, n_blocks;
-  int max_nodes, Hq, Hkv, group, nsplit, ntail, split, lane_len, stages, per_cta;
+  int B, max_nodes, Hq, Hkv, group, gshift, nsplit, ntail, split, lane_len, stages;
   float scale_log2;
   float neg_zero;  // -0, see mul2
 };
@@ -409,7 +409,9 @@ __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(const TreeAr
 }
 
 // ------------------------------------------------------------------------ the lanes before E
-// A CTA owns (sequence, tile of 128 rows, kv head) and up to per_cta splits.  S = Q K^T (K = hd in 16-wide steps,
+// A unit is (sequence, kv head, tile of 128 rows, split), numbered in that order; every CTA takes an equal run of the
+// call's units, so contexts of any lengths spread evenly and a CTA's consecutive splits of one row tile go through
+// one pipeline.  S = Q K^T (K = hd in 16-wide steps,
 // ascending) and O = P V (64 keys in 16-wide steps, ascending) accumulate in TMEM; tcgen05.mma and mma.sync give
 // the same fp32 bits for the same 16-wide steps.  A softmax thread holds one row: its 64 scores of a tile, and the
 // split's running state in registers.  P goes back to TMEM, over the scores it came from, as the A operand of P V.
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(const TreeAr
 // roundings).  S of a tile is computed while the one before it is in the softmax, and the accumulator of a finished
 // lane is folded while the next lane's first scores are.
 // Two CTAs share an SM (their chains softmax -> P V -> fold interleave): 114 KB of shared memory and 256 TMEM
-// columns each, and 128 registers a thread at launch, which the warpgroups then split 232 to 24.
+// columns each, and 128 registers a thread at launch, which the warpgroups then split 224 to 32.
 template <int HD>
 struct CtxLayout {
   static constexpr int kQ = 128 * HD * 2;       // HD/64 boxes of 128 rows x 128 bytes
@@ -426,9 +428,9 @@ struct CtxLayout {
   static constexpr int kSlots = HD == 128 ? 5 : 11;
   static constexpr int kOffKV = kQ;
   static constexpr int kOffBar = kOffKV + kSlots * kPage;
-  static constexpr int kBytes = kOffBar + 512;
+  static constexpr int kBytes = kOffBar + 640;
   static constexpr int kThreads = 256;
-  static constexpr int kSoftmaxRegs = 232, kOtherRegs = 24, kLaunchRegs = 128;
+  static constexpr int kSoftmaxRegs = 224, kOtherRegs = 32, kLaunchRegs = 128;
   static_assert(128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
   static constexpr uint32_t kCols = 256, kColS = 0, kColO = 128;  // S0, S1 (64 each; P over them), O (HD)
 };
@@ -440,6 +442,13 @@ BI_DEV void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uin
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// One lane of the (converged) warp.  The compiler knows that a branch on it has one thread: tcgen05.mma then issues in
+// 55-80 clocks, against 200 in a branch on lane == 0 (whatever N and the accumulator: M = 128, N = 32..128).
+BI_DEV bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
 }
 // Two products, each rounded once: x y + nz with nz = (-0, -0), a value that the compiler cannot see.  (It contracts
 // mul.rn.f32x2 and a following add.rn.f32x2 into one rounding.)
@@ -460,6 +469,55 @@ BI_DEV float2 add2(float2 x, float2 y) {
   return r;
 }
 
+// A CTA's place in the call's units: those of one (sequence, kv head, row tile) from split s on, and the rest of the run.
+struct CtxCursor {
+  TreeSeq sq;
+  int b, kvh, tile, s;
+  int n_split, n_tile;  // splits with lanes before E, and row tiles, of the sequence
+  int64_t left;         // units of the CTA from here on
+  // the sequence's units: n_split and n_tile of it are set
+  BI_DEV int64_t sequence(const TreeArgs& a, int b_) {
+    b = b_;
+    sq = tree_seq(a, b);
+    const int E = sq.ok ? tail_lane(a, sq.start) : 0;
+    n_split = min((E + a.split - 1) / a.split, a.nsplit);
+    n_tile = ((sq.n << a.gshift) + 127) >> 7;
+    return (int64_t)n_split * n_tile * a.Hkv;
+  }
+  BI_DEV void at(int64_t v) {  // unit v of the sequence
+    s = (int)(v % n_split);
+    const int64_t w = v / n_split;
+    tile = (int)(w % n_tile);
+    kvh = (int)(w / n_tile);
+  }
+  BI_DEV int splits() const { return (int)min((int64_t)(n_split - s), left); }  // of this row tile
+  // 64-key tiles of `splits()` splits from s on
+  BI_DEV int tiles(const TreeArgs& a) const {
+    const int E = tail_lane(a, sq.start);
+    return (min(E, (s + splits()) * a.split) - s * a.split) / kKeys;
+  }
+  BI_DEV void next(const TreeArgs& a) {  // past this row tile's splits
+    left -= splits();
+    s = 0;
+    if (++tile == n_tile) {
+      tile = 0;
+      ++kvh;
+    }
+    while (left > 0 && kvh == a.Hkv && b + 1 < a.B)
+      if (sequence(a, b + 1) > 0) kvh = 0;
+    if (kvh == a.Hkv) left = 0;
+  }
+};
+
+// A row tile's consecutive splits, as the producer hands them to the other warps.
+struct CtxSegment {
+  int64_t row0;      // of the sequence
+  int n, s0, s_end;  // 64-key tiles (0: the run has ended); splits s0 .. s_end - 1
+  int r0, n_rows;    // the tile's first row, and the sequence's rows
+  int head0;         // the kv head's first q head
+};
+constexpr int kSegments = 4;  // in flight
+
 template <int HD>
 __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
     tree_context_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk,
@@ -475,30 +533,19 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
   uint64_t* s_full = kv_empty + NS;  // [2] MMA -> softmax: S of a tile is in TMEM
   uint64_t* p_full = s_full + 2;     // softmax -> MMA: P written, O folded or rescaled (4 warp arrivals)
   uint64_t* o_done = p_full + 1;     // MMA -> softmax, MMA: P V of a tile has completed
-  uint64_t* q_full = o_done + 1;     // softmax -> MMA: Q tile loaded (128 thread arrivals)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 1);
+  uint64_t* q_full = o_done + 1;     // softmax -> MMA: Q of a row tile loaded (128 thread arrivals)
+  uint64_t* seg_full = q_full + 1;   // [kSegments] TMA -> all: a segment stands in its place
+  uint64_t* seg_empty = seg_full + kSegments;  // [kSegments] read (MMA thread and 4 warps)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_empty + kSegments);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* first_b = reinterpret_cast<int*>(tmem_slot + 2);
+  int64_t* first_v = reinterpret_cast<int64_t*>(tmem_slot + 4);
+  int64_t* sums = first_v + 1;  // [8]
+  CtxSegment* segs = reinterpret_cast<CtxSegment*>(sums + 8);
+  static_assert((2 * NS + 5 + 2 * kSegments) * 8 + 16 + 72 + kSegments * sizeof(CtxSegment) <= Lay::kBytes - Lay::kOffBar,
+                "barriers and segments fit");
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b = blockIdx.y;
-  const int kvh = blockIdx.z % a.Hkv;
-  const int s0 = (blockIdx.z / a.Hkv) * a.per_cta;  // first split of this CTA
-  // The launch before this one (tree_tail_kernel) starts it only after its own predecessors have completed, so q, the
-  // caches and the tables may be read at once (through L2, where those wrote them); what ends below waits for it.
-  const TreeSeq sq = tree_seq(a, b);
-  const int64_t r_first = (int64_t)blockIdx.x * 128;
-  const int64_t n_rows = sq.ok ? (int64_t)sq.n * a.group : 0;
-  int n_tiles = 0;
-  const int ntf = a.split / kKeys;  // tiles of a whole split; tile k is tile k % ntf of split s0 + k / ntf
-  if (r_first < n_rows) {
-    const int E = tail_lane(a, sq.start);
-    const int last = min(s0 + a.per_cta, a.nsplit) * a.split;  // exclusive
-    n_tiles = max(0, min(E, last) - s0 * a.split) / kKeys;
-  }
-  if (n_tiles == 0) {
-    pdl_wait();
-    return;
-  }
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&kv_full[i], 1);
@@ -509,7 +556,12 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
     mbar_init(p_full, 4);
     mbar_init(o_done, 1);
     mbar_init(q_full, 128);
+    for (int i = 0; i < kSegments; ++i) {
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], 5);
+    }
     *abort_flag = 0;
+    *first_b = -1;
     fence_barrier_init();
   }
   if (warp == kWarpMma) {
@@ -517,48 +569,119 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
     tmem_relinquish();
   }
   tc_fence_before();
+  // The launch before this one (tree_tail_kernel) starts it only after its own predecessors have completed, so q, the
+  // caches and the tables may be read at once (through L2, where those wrote them); the end waits for it.
+  CtxCursor cur;
+  // the sum of a 256-sequence group's units over the threads before this one, and over all
+  auto scan = [&](int64_t mine, int64_t& all) {
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    int64_t before = inc - mine;
+    all = 0;
+    for (int w = 0; w < 8; ++w) {
+      before += w < warp ? sums[w] : 0;
+      all += sums[w];
+    }
+    return before;
+  };
+  int64_t total = 0, mine0 = 0, before0 = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 256) {
+    const int64_t mine = b0 + tid < a.B ? cur.sequence(a, b0 + tid) : 0;
+    int64_t all;
+    const int64_t before = scan(mine, all);
+    if (b0 == 0) mine0 = mine, before0 = before;
+    total += all;
+  }
+  const int64_t u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+  int64_t run_up = 0;
+  for (int b0 = 0; b0 < a.B && u0 < u1; b0 += 256) {
+    int64_t mine = mine0, before = before0, all = total;
+    if (a.B > 256) {
+      mine = b0 + tid < a.B ? cur.sequence(a, b0 + tid) : 0;
+      before = scan(mine, all);
+    }
+    if (run_up + before <= u0 && u0 < run_up + before + mine) {
+      *first_b = b0 + tid;
+      *first_v = u0 - run_up - before;
+    }
+    run_up += all;
+    if (run_up > u0) break;
+  }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_trigger();
   const int tpl = a.lane_len / kKeys;  // tiles of a lane
+  const int ntf = a.split / kKeys;     // and of a whole split
 
   if (warp >= 4) {
     reg_alloc_dec<Lay::kOtherRegs>();
-    if (warp == kWarpTma && lane == 0) {
+    if (warp == kWarpTma && elect_one()) {
       // ---------------- TMA producer: K and V pages in order
       const int rows_total = (int)(a.n_blocks * a.Hkv * kKeys);
-      const int32_t* bt = a.block_table + (int64_t)b * a.max_blk;
-      const int page0 = s0 * ntf;
+      cur.left = *first_b < 0 ? 0 : u1 - u0;
+      if (cur.left > 0) {
+        cur.sequence(a, *first_b);
+        cur.at(*first_v);
+      }
       int i = 0;
-      int32_t blk = page0 < a.max_blk ? __ldcg(bt + page0) : -1;
-      for (int t = 0; t < n_tiles && !*abort_flag; ++t) {
-        int row = rows_total;  // past the end: the copy reads zeros
-        if (blk >= 0 && blk < a.n_blocks) row = (int)(((int64_t)blk * a.Hkv + kvh) * kKeys);
-        else report(a.status, DEV_BAD_INDEX);
-        if (t + 1 < n_tiles) blk = page0 + t + 1 < a.max_blk ? __ldcg(bt + page0 + t + 1) : -1;
-        for (int v = 0; v < 2 && !*abort_flag; ++v) {
-          const int slot = i % NS;
-          if (i >= NS && !mbar_wait(&kv_empty[slot], ((i / NS) - 1) & 1)) {
-            report(a.status, DEV_TIMEOUT);
-            *abort_flag = 1;
-            break;
-          }
-          uint8_t* dst = sKV + slot * Lay::kPage;
-          mbar_arrive_expect_tx(&kv_full[slot], Lay::kPage);
+      for (int q = 0; !*abort_flag; ++q, cur.next(a)) {
+        const int place = q % kSegments;
+        if (q >= kSegments && !mbar_wait(&seg_empty[place], ((q / kSegments) - 1) & 1)) {
+          report(a.status, DEV_TIMEOUT);
+          *abort_flag = 1;
+        }
+        segs[place].n = cur.left > 0 ? cur.tiles(a) : 0;
+        if (cur.left > 0) {
+          segs[place].row0 = cur.sq.row0;
+          segs[place].s0 = cur.s;
+          segs[place].s_end = cur.s + cur.splits();
+          segs[place].r0 = cur.tile * 128;
+          segs[place].n_rows = cur.sq.n << a.gshift;
+          segs[place].head0 = cur.kvh * a.group;
+        }
+        mbar_arrive(&seg_full[place]);
+        if (cur.left <= 0) break;
+        const int32_t* bt = a.block_table + (int64_t)cur.b * a.max_blk;
+        const int page0 = cur.s * ntf, page1 = page0 + cur.tiles(a);
+        int32_t blk = page0 < a.max_blk ? __ldcg(bt + page0) : -1;
+        for (int page = page0; page < page1 && !*abort_flag; ++page) {
+          int row = rows_total;  // past the end: the copy reads zeros
+          if (blk >= 0 && blk < a.n_blocks) row = (int)(((int64_t)blk * a.Hkv + cur.kvh) * kKeys);
+          else report(a.status, DEV_BAD_INDEX);
+          if (page + 1 < page1) blk = page + 1 < a.max_blk ? __ldcg(bt + page + 1) : -1;
+          for (int v = 0; v < 2 && !*abort_flag; ++v) {
+            const int slot = i % NS;
+            if (i >= NS && !mbar_wait(&kv_empty[slot], ((i / NS) - 1) & 1)) {
+              report(a.status, DEV_TIMEOUT);
+              *abort_flag = 1;
+              break;
+            }
+            uint8_t* dst = sKV + slot * Lay::kPage;
+            mbar_arrive_expect_tx(&kv_full[slot], Lay::kPage);
 #pragma unroll
-          for (int x = 0; x < HD / 64; ++x)
-            tma_load_2d(dst + x * (kKeys * 128), v ? &tmv : &tmk, &kv_full[slot], x * 64, row);
-          ++i;
+            for (int x = 0; x < HD / 64; ++x)
+              tma_load_2d(dst + x * (kKeys * 128), v ? &tmv : &tmk, &kv_full[slot], x * 64, row);
+            ++i;
+          }
         }
       }
       // the copies this CTA started land before it can exit
       for (int k = 0; k < NS && k < i; ++k) mbar_wait(&kv_full[(i - 1 - k) % NS], ((i - 1 - k) / NS) & 1);
-    } else if (warp == kWarpMma && lane == 0) {
+    } else if (warp == kWarpMma && elect_one()) {
       // ---------------- MMA issuer
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, kKeys);
       constexpr uint32_t idesc_o = idesc_bf16_f32(128, HD) | (1u << 16);  // V read MN-major
-      bool ok = mbar_wait(q_full, 0);
+      int t = 0;        // tiles so far
+      bool ok = true;
+      int seg = 0;      // row tiles so far
       auto issue_s = [&](int t) -> bool {
         const int i = 2 * t;
         if (!mbar_wait(&kv_full[i % NS], (i / NS) & 1)) return false;
@@ -574,28 +697,38 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
         tc_commit(&kv_empty[i % NS]);
         return true;
       };
-      if (ok) ok = issue_s(0);
-      for (int t = 0; ok && t < n_tiles && !*abort_flag; ++t) {
-        // S of tile t + 1 takes the columns that hold P of tile t - 1
-        if (t + 1 < n_tiles && ((t > 0 && !mbar_wait(o_done, (t - 1) & 1)) || !issue_s(t + 1))) {
-          ok = false;
-          break;
-        }
-        const int i = 2 * t + 1;
-        if (!mbar_wait(p_full, t & 1) || !mbar_wait(&kv_full[i % NS], (i / NS) & 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t va = smem_u32(sKV + i % NS * Lay::kPage);
-        const bool fresh = t % ntf % tpl == 0;  // a lane's first tile starts from nothing
+      for (; ok && !*abort_flag; ++seg) {
+        const int place = seg % kSegments;
+        if (!(ok = mbar_wait(&seg_full[place], (seg / kSegments) & 1))) break;
+        const int n = segs[place].n;
+        mbar_arrive(&seg_empty[place]);
+        if (n == 0) break;
+        // S of tile t takes the columns that hold P of tile t - 2, whose P V the softmax had seen done before it gave
+        // out P of tile t - 1
+        ok = mbar_wait(q_full, seg & 1) && issue_s(t);
+        int i_split = 0, i_lane = 0;
+        for (int k = 0; ok && k < n && !*abort_flag; ++k, ++t) {
+          if (k + 1 < n && ((t > 0 && !mbar_wait(o_done, (t - 1) & 1)) || !issue_s(t + 1))) {
+            ok = false;
+            break;
+          }
+          const int i = 2 * t + 1;
+          if (!mbar_wait(p_full, t & 1) || !mbar_wait(&kv_full[i % NS], (i / NS) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t va = smem_u32(sKV + i % NS * Lay::kPage);
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          tc_mma_bf16_ts(tmem + Lay::kColO, tmem + Lay::kColS + (t & 1) * kKeys + k * 8,
-                         sw128_mnmajor_desc(va + k * 16 * 128, kKeys * 128, 1024), idesc_o,
-                         k == 0 && fresh ? 0u : 1u);
-        tc_commit(o_done);
-        tc_commit(&kv_empty[i % NS]);
+          for (int x = 0; x < kKeys / 16; ++x)  // a lane's first tile starts from nothing
+            tc_mma_bf16_ts(tmem + Lay::kColO, tmem + Lay::kColS + (t & 1) * kKeys + x * 8,
+                           sw128_mnmajor_desc(va + x * 16 * 128, kKeys * 128, 1024), idesc_o,
+                           x == 0 && i_lane == 0 ? 0u : 1u);
+          tc_commit(o_done);
+          tc_commit(&kv_empty[i % NS]);
+          if (++i_lane == tpl) i_lane = 0;
+          if (++i_split == ntf) i_split = i_lane = 0;
+        }
       }
       if (!ok) {
         report(a.status, DEV_TIMEOUT);
@@ -605,23 +738,40 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
   } else {
     reg_alloc_inc<Lay::kSoftmaxRegs>();
     // ---------------- softmax: thread tid holds row tid of the tile (its TMEM lane)
-    for (int i = tid; i < 128 * (HD / 8); i += 128) {
-      const int qrow = i / (HD / 8), ch = i % (HD / 8);
-      const int64_t r = r_first + qrow;
-      const bool valid = r < n_rows;
-      const __nv_bfloat16* src =
-          a.q + ((sq.row0 + r / a.group) * a.Hq + kvh * a.group + r % a.group) * HD + ch * 8;
-      cp_async16(sQ + (ch >> 3) * (128 * 128) + qrow * 128 + (((ch & 7) ^ (qrow & 7)) << 4), valid ? src : a.q, valid);
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    fence_proxy_async();
-    mbar_arrive(q_full);
-
-    const int64_t r = r_first + tid;
-    const bool valid = r < n_rows;
-    const bool live = r_first + warp * 32 < n_rows;  // the warp has rows
-    const int64_t rec0 = valid ? ((sq.row0 + r / a.group) * a.Hq + kvh * a.group + r % a.group) * a.nsplit : 0;
+    int seg_n = 0, seg_q = 0;  // tiles of the segment at hand; segments so far
+    int64_t seg_rec = 0;       // this thread's row in it, as an index of q heads; -1: none
+    int seg_s0 = 0, seg_end = 0;
+    bool seg_live = false;     // a row of the warp exists
+    // the next segment: its numbers, and its Q on the way to shared memory
+    auto next_segment = [&]() -> bool {
+      const int place = seg_q % kSegments;
+      if (!__all_sync(0xffffffffu, mbar_wait(&seg_full[place], (seg_q / kSegments) & 1))) return false;
+      const CtxSegment g = segs[place];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[place]);
+      ++seg_q;
+      seg_n = g.n;
+      if (g.n == 0) return true;
+      seg_s0 = g.s0;
+      seg_end = g.s_end;
+      seg_live = g.r0 + warp * 32 < g.n_rows;
+      auto index = [&](int r) { return (g.row0 + (r >> a.gshift)) * a.Hq + g.head0 + (r & (a.group - 1)); };
+      seg_rec = g.r0 + tid < g.n_rows ? index(g.r0 + tid) : -1;
+#pragma unroll 4
+      for (int i = tid; i < 128 * (HD / 8); i += 128) {
+        const int qrow = i / (HD / 8), ch = i % (HD / 8);
+        const bool there = g.r0 + qrow < g.n_rows;
+        cp_async16(sQ + (ch >> 3) * (128 * 128) + qrow * 128 + (((ch & 7) ^ (qrow & 7)) << 4),
+                   there ? a.q + index(g.r0 + qrow) * HD + ch * 8 : a.q, there);
+      }
+      cp_async_commit();
+      return true;
+    };
+    auto q_ready = [&] {
+      cp_async_wait<0>();
+      fence_proxy_async();
+      mbar_arrive(q_full);
+    };
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     const uint32_t tO = tmem + lane_base + Lay::kColO;
     const float nz = a.neg_zero;
@@ -629,6 +779,7 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
 #pragma unroll
     for (int c = 0; c < HD; ++c) run[c] = 0.f;
     float m = -INFINITY, l = 0.f;  // the lane in progress
+    int64_t rec0 = -1;             // the row's records
 
     // run <- run (+) (lm, ll, O): lane_merge's formula, an empty run taking O as it is (0 * 0 + O * 1).  The last lane
     // of a split: the result is split s's record, and run starts over (s < 0: none).
@@ -667,106 +818,127 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
           float4* po = reinterpret_cast<float4*>(a.part_o + (rec0 + s) * HD + c);
 #pragma unroll
           for (int k = 0; k < 32; k += 4) {
-            if (valid) po[k / 4] = make_float4(run[c + k], run[c + k + 1], run[c + k + 2], run[c + k + 3]);
+            if (rec0 >= 0) po[k / 4] = make_float4(run[c + k], run[c + k + 1], run[c + k + 2], run[c + k + 3]);
             run[c + k] = run[c + k + 1] = run[c + k + 2] = run[c + k + 3] = 0.f;
           }
         }
       }
       if (s >= 0) {
-        if (valid) *reinterpret_cast<float2*>(a.part_ml + (rec0 + s) * 2) = make_float2(run_m, run_l);
+        if (rec0 >= 0) *reinterpret_cast<float2*>(a.part_ml + (rec0 + s) * 2) = make_float2(run_m, run_l);
         run_m = -INFINITY;
         run_l = 0.f;
       }
     };
-    bool ok = true;
-    int i_split = 0, i_lane = 0;  // tile t is tile i_split of its split, i_lane of its lane
-    for (int t = 0; t < n_tiles; ++t) {
-      ok = mbar_wait(&s_full[t & 1], (t >> 1) & 1);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      const bool fresh = i_lane == 0;
-      float alpha = 1.f;
-      const float lm = m, ll = l;  // of the lane before, when this tile starts one
-      if (live) {
-        const uint32_t tS = tmem + lane_base + Lay::kColS + (t & 1) * kKeys;
-        uint32_t s[64];
-        tmem_ld_32x32b_x32(tS, *reinterpret_cast<uint32_t (*)[32]>(&s[0]));
-        tmem_ld_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t (*)[32]>(&s[32]));
-        tmem_ld_wait();
-        // the largest score is the largest product's (scale > 0 and rounding is monotone)
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int k = 0; k < 64; k += 2)
-          mx[(k >> 1) & 3] = fmaxf(mx[(k >> 1) & 3], fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
-        const float top = __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.scale_log2);
-        const float m_old = fresh ? -INFINITY : m;
-        const float m_new = fmaxf(m_old, top);
-        alpha = m_new == m_old ? 1.0f : exp2f(__fsub_rn(m_old, m_new));
-        const float2 sc = make_float2(a.scale_log2, a.scale_log2);
-        // a row without any key above -inf so far: 2^(-inf - 0) = 0
-        const float neg = m_new == -INFINITY ? 0.f : -m_new;
-        const float2 ng = make_float2(neg, neg);
-        float2 s01 = make_float2(0.f, 0.f), s23 = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int h = 0; h < 64; h += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            float p[8];
-#pragma unroll
-            for (int k = 0; k < 8; k += 2) {
-              const float2 x = add2(
-                  mul2(make_float2(__uint_as_float(s[h + j + k]), __uint_as_float(s[h + j + k + 1])), sc, nz), ng);
-              p[k] = exp2_p(x.x);
-              p[k + 1] = exp2_p(x.y);
-              pk[(j + k) / 2] = pack_bf16x2(p[k], p[k + 1]);
-            }
-            s01 = add2(add2(s01, make_float2(p[0], p[2])), make_float2(p[1], p[3]));
-            s23 = add2(add2(s23, make_float2(p[4], p[6])), make_float2(p[5], p[7]));
-          }
-          tmem_st_32x32b_x16(tS + h / 2, pk);
-        }
-        const float rs = __fadd_rn(__fadd_rn(s01.x, s01.y), __fadd_rn(s23.x, s23.y));
-        l = __fadd_rn(__fmul_rn(fresh ? 0.f : l, alpha), rs);
-        m = m_new;
-      }
-      if (t > 0) {
-        ok = mbar_wait(o_done, (t - 1) & 1);
+
+    int t = 0;  // tiles so far
+    bool ok = next_segment();
+    if (ok && seg_n > 0) q_ready();
+    while (ok && seg_n > 0) {
+      const int n = seg_n, s0 = seg_s0, s_last = seg_end - 1;
+      const bool live = seg_live;
+      rec0 = seg_rec < 0 ? -1 : seg_rec * a.nsplit;
+      int i_split = 0, i_lane = 0, split = s0;  // the tile's place in its split and lane
+      for (int k = 0; k < n; ++k, ++t) {
+        ok = mbar_wait(&s_full[t & 1], (t >> 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        if (live && fresh) {
-          fold(lm, ll, i_split == 0 ? s0 + (t - 1) / ntf : -1);
-        } else if (live && __any_sync(0xffffffffu, alpha != 1.0f)) {
-          const float2 al = make_float2(alpha, alpha);
+        const bool fresh = i_lane == 0;
+        float alpha = 1.f;
+        const float lm = m, ll = l;  // of the lane before, when this tile starts one
+        if (k + 1 == n && !(ok = next_segment())) break;  // the last S of the row tile is there: Q may go
+        if (live) {
+          const uint32_t tS = tmem + lane_base + Lay::kColS + (t & 1) * kKeys;
+          uint32_t s[64];
+          tmem_ld_32x32b_x32(tS, *reinterpret_cast<uint32_t (*)[32]>(&s[0]));
+          tmem_ld_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t (*)[32]>(&s[32]));
+          tmem_ld_wait();
+          // the largest score is the largest product's (scale > 0 and rounding is monotone)
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < HD; c += 32) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(tO + c, o);
-            tmem_ld_wait();
+          for (int j = 0; j < 64; j += 2)
+            mx[(j >> 1) & 3] = fmaxf(mx[(j >> 1) & 3], fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
+          const float top = __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.scale_log2);
+          const float m_old = fresh ? -INFINITY : m;
+          const float m_new = fmaxf(m_old, top);
+          alpha = m_new == m_old ? 1.0f : exp2f(__fsub_rn(m_old, m_new));
+          const float2 sc = make_float2(a.scale_log2, a.scale_log2);
+          // a row without any key above -inf so far: 2^(-inf - 0) = 0
+          const float neg = m_new == -INFINITY ? 0.f : -m_new;
+          const float2 ng = make_float2(neg, neg);
+          float2 s01 = make_float2(0.f, 0.f), s23 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              const float2 x = mul2(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), al, nz);
-              o[k] = __float_as_uint(x.x);
-              o[k + 1] = __float_as_uint(x.y);
+          for (int h = 0; h < 64; h += 32) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              float p[8];
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) {
+                const float2 x = add2(
+                    mul2(make_float2(__uint_as_float(s[h + j + e]), __uint_as_float(s[h + j + e + 1])), sc, nz), ng);
+                p[e] = exp2_p(x.x);
+                p[e + 1] = exp2_p(x.y);
+                pk[(j + e) / 2] = pack_bf16x2(p[e], p[e + 1]);
+              }
+              s01 = add2(add2(s01, make_float2(p[0], p[2])), make_float2(p[1], p[3]));
+              s23 = add2(add2(s23, make_float2(p[4], p[6])), make_float2(p[5], p[7]));
             }
-            tmem_st_32x32b_x32(tO + c, o);
+            tmem_st_32x32b_x16(tS + h / 2, pk);
+          }
+          const float rs = __fadd_rn(__fadd_rn(s01.x, s01.y), __fadd_rn(s23.x, s23.y));
+          l = __fadd_rn(__fmul_rn(fresh ? 0.f : l, alpha), rs);
+          m = m_new;
+        }
+        if (k > 0) {
+          ok = mbar_wait(o_done, (t - 1) & 1);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc_fence_after();
+          if (live && fresh) {
+            fold(lm, ll, i_split == 0 ? split - 1 : -1);
+          } else if (live && __any_sync(0xffffffffu, alpha != 1.0f)) {
+            const float2 al = make_float2(alpha, alpha);
+#pragma unroll
+            for (int c = 0; c < HD; c += 32) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(tO + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float2 x = mul2(make_float2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])), al, nz);
+                o[j] = __float_as_uint(x.x);
+                o[j + 1] = __float_as_uint(x.y);
+              }
+              tmem_st_32x32b_x32(tO + c, o);
+            }
           }
         }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+        if (++i_lane == tpl) i_lane = 0;
+        if (++i_split == ntf) {
+          i_split = i_lane = 0;
+          ++split;
+        }
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
-      if (++i_lane == tpl) i_lane = 0;
-      if (++i_split == ntf) i_split = i_lane = 0;
-    }
-    if (ok && __all_sync(0xffffffffu, ok)) ok = mbar_wait(o_done, (n_tiles - 1) & 1);
-    if (__all_sync(0xffffffffu, ok)) {
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      if (seg_n > 0) q_ready();
+      ok = mbar_wait(o_done, (t - 1) & 1);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
       tc_fence_after();
-      if (live) fold(m, l, s0 + (n_tiles - 1) / ntf);
-    } else {
+      if (live) fold(m, l, s_last);
+    }
+    if (!ok) {
       if (lane == 0) report(a.status, DEV_TIMEOUT);
       *abort_flag = 1;
+      cp_async_wait<0>();
     }
     tc_fence_before();
   }
@@ -947,10 +1119,9 @@ static bi_status launch_tree(TreeArgs args, int64_t B, cudaStream_t st) {
                              dim3((unsigned)cdiv(args.max_nodes, per_cta), (unsigned)B, (unsigned)args.Hkv),
                              dim3(kTailWarps * 32), Tail::bytes(args.stages), st, args, tmk, tmv),
                   "tree_tail_kernel"));
-  args.per_cta = 1;
-  BI_TRY(launched(launch_pdl(tree_context_kernel<HD>,
-                             dim3((unsigned)cdiv(r, 128), (unsigned)B,
-                                  (unsigned)(args.Hkv * cdiv(args.nsplit, args.per_cta))),
+  // at most one CTA a unit, and what fits on the GPU at once
+  const int64_t units = cdiv(r, 128) * B * args.Hkv * args.nsplit;
+  BI_TRY(launched(launch_pdl(tree_context_kernel<HD>, dim3((unsigned)std::min<int64_t>(units, 2 * (int64_t)num_sms())),
                              dim3(Ctx::kThreads), Ctx::kBytes, st, args, tmk, tmv),
                   "tree_context_kernel"));
   return launched(launch_pdl(tree_merge_kernel<HD>,
@@ -1022,12 +1193,15 @@ bi_status bi_tree_attention(const void* q, int64_t T, const int32_t* parent, con
   a.max_nodes = (int)max_nodes;
   a.Hq = Hq;
   a.Hkv = Hkv;
-  a.group = group;
+  a.B = (int)B;
+  a.group = group;  // a power of two (a divisor of 64)
+  a.gshift = 0;
+  while ((1 << a.gshift) < group) ++a.gshift;
   a.nsplit = (int)ns;
   a.ntail = nt;
   a.lane_len = lane_len;
   a.split = kv_split;
-  a.stages = a.per_cta = 0;
+  a.stages = 0;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.neg_zero = -0.f;
   return hd == 64 ? launch_tree<64>(a, B, as_stream(stream)) : launch_tree<128>(a, B, as_stream(stream));
