@@ -443,6 +443,14 @@ BI_DEV void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uin
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// A tile of K or V; `policy` is its L2 eviction priority.
+BI_DEV void tma_load_2d_hint(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4}], "
+      "[%2], %5;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "l"(policy)
+      : "memory");
+}
 // One lane of the (converged) warp.  The compiler knows that a branch on it has one thread: tcgen05.mma then issues in
 // 55-80 clocks, against 200 in a branch on lane == 0 (whatever N and the accumulator: M = 128, N = 32..128).
 BI_DEV bool elect_one() {
@@ -626,6 +634,9 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
     if (warp == kWarpTma && elect_one()) {
       // ---------------- TMA producer: K and V pages in order
       const int rows_total = (int)(a.n_blocks * a.Hkv * kKeys);
+      // the records are read back by the merge, the pages only by a neighbouring CTA at about the same time
+      uint64_t policy;
+      asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
       cur.left = *first_b < 0 ? 0 : u1 - u0;
       if (cur.left > 0) {
         cur.sequence(a, *first_b);
@@ -668,7 +679,7 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
             mbar_arrive_expect_tx(&kv_full[slot], Lay::kPage);
 #pragma unroll
             for (int x = 0; x < HD / 64; ++x)
-              tma_load_2d(dst + x * (kKeys * 128), v ? &tmv : &tmk, &kv_full[slot], x * 64, row);
+              tma_load_2d_hint(dst + x * (kKeys * 128), v ? &tmv : &tmk, &kv_full[slot], x * 64, row, policy);
             ++i;
           }
         }
@@ -949,113 +960,120 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
 }
 
 // ------------------------------------------------------------------------ the merge
-// A warp a (node, q head), HD / 32 elements a lane.  The splits before E are merged as the attention merge does
-// (weights by lane, sums in ascending order); the split that E cuts and those behind it are first folded from their
-// lanes with lane_merge's formula.
+// A warp a (node, q head), HD / 32 neighbouring elements a lane.  The splits before E are merged as the attention merge
+// does (a weight a lane, 32 at a time; sums in ascending order; places behind the last split add 0 * 0, and the sums,
+// which start from +0, are never -0); the split that E cuts and those behind it are first folded from their lanes with
+// lane_merge's formula.  Loads that do not depend on the row's position go out at once, and the next 8 records while
+// 8 are added up.
 constexpr int kTreeMergeWarps = 4;
+constexpr int kTreeMergeBatch = 8;
 
 template <int HD>
 __global__ void __launch_bounds__(kTreeMergeWarps * 32) tree_merge_kernel(const TreeArgs a) {
+  constexpr int NE = HD / 32, NB = kTreeMergeBatch;
+  __shared__ float2 weights[kTreeMergeWarps][32];  // (weight, l) of 32 splits
   pdl_trigger();
   pdl_wait();
-  constexpr int NE = HD / 32;
-  const int lane = threadIdx.x & 31;
+  struct Vec {
+    float v[NE];
+  };
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.y, i = blockIdx.x;
-  const int head = blockIdx.z * kTreeMergeWarps + (threadIdx.x >> 5);
+  const int head = blockIdx.z * kTreeMergeWarps + warp;
   if (head >= a.Hq) return;
   const TreeSeq sq = tree_seq(a, b);
   if (i >= sq.n) return;
   const int64_t row = sq.row0 + i;
   const int pos = __ldcg(a.row_pos + row);
-  __nv_bfloat16* dst = a.out + (row * a.Hq + head) * HD + lane * NE;
-  struct Vec {
-    float v[NE];
-  };
-  auto load = [&](const float* p) {
-    Vec r;
+  auto load = [&](const float* p, bool there) {
+    Vec r = {};
     if constexpr (NE == 4) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(p + lane * 4));
+      const float4 x = there ? __ldcg(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
       r.v[0] = x.x, r.v[1] = x.y, r.v[2] = x.z, r.v[3] = x.w;
     } else {
-      const float2 x = __ldcg(reinterpret_cast<const float2*>(p + lane * 2));
+      const float2 x = there ? __ldcg(reinterpret_cast<const float2*>(p)) : make_float2(0.f, 0.f);
       r.v[0] = x.x, r.v[1] = x.y;
     }
     return r;
   };
-  auto store = [&](const Vec& r) {
+  const bool ok = sq.ok;
+  const int E = ok ? tail_lane(a, sq.start) : 0;
+  const int sE = ok ? min(sq.start / a.split, a.nsplit) : 0;  // the split that E stands in
+  const bool cut = E > sE * a.split && sE < a.nsplit;         // with lanes before E in it
+  const int64_t rec = row * a.Hq + head;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + rec * a.nsplit;
+  const float2* tml = reinterpret_cast<const float2*>(a.tail_ml) + rec * a.ntail;
+  const float* po = a.part_o + rec * a.nsplit * HD + lane * NE;
+  const float* to = a.tail_o + rec * a.ntail * HD + lane * NE;
+  const float2 none = make_float2(-INFINITY, 0.f);
+  float2 r = lane < sE ? __ldcg(ml + lane) : none;
+  const float2 rc = cut ? __ldcg(ml + sE) : none;
+  const float2 rt = lane < a.ntail ? __ldcg(tml + lane) : none;
+  Vec v[NB];
+#pragma unroll
+  for (int k = 0; k < NB; ++k) v[k] = load(po + (int64_t)k * HD, k < sE);
+  Vec P = load(po + (int64_t)sE * HD, cut);
+  Vec Q = load(to, true);
+  __nv_bfloat16* dst = a.out + rec * HD + lane * NE;
+  auto store = [&](const Vec& x) {
     uint32_t w[NE / 2];
 #pragma unroll
-    for (int e = 0; e < NE; e += 2) w[e / 2] = pack_bf16x2(r.v[e], r.v[e + 1]);
+    for (int e = 0; e < NE; e += 2) w[e / 2] = pack_bf16x2(x.v[e], x.v[e + 1]);
     if constexpr (NE == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(dst) = w[0];
   };
   Vec O = {};
-  if (pos < 0) {
+  if (!ok || pos < 0) {
     store(O);
     return;
   }
-  const int E = tail_lane(a, sq.start);
-  const int sE = sq.start / a.split;           // the split that E stands in
-  const bool cut = E > sE * a.split;           // with lanes before E in it
-  const int64_t rec = row * a.Hq + head;
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + rec * a.nsplit;
-  const float2* tml = reinterpret_cast<const float2*>(a.tail_ml) + rec * a.ntail;
-  const float* po = a.part_o + rec * a.nsplit * HD;
-  const float* to = a.tail_o + rec * a.ntail * HD;
-  const int n_ctx = sE + (cut ? 1 : 0);        // records before E
   // the largest score
-  float M = -INFINITY;
-  for (int s = lane; s < n_ctx; s += 32) M = fmaxf(M, __ldcg(ml + s).x);
   int n_tail = 0;
-  for (int lb = E; lb <= pos && n_tail < a.ntail; lb = lane_end(a, lb)) {
-    if (lane == 0) M = fmaxf(M, __ldcg(tml + n_tail).x);
-    ++n_tail;
-  }
+  for (int lb = E; lb <= pos && n_tail < a.ntail; lb = lane_end(a, lb)) ++n_tail;
+  float M = fmaxf(r.x, rc.x);
+  if (lane < n_tail) M = fmaxf(M, rt.x);
+  for (int t = 32 + lane; t < n_tail; t += 32) M = fmaxf(M, __ldcg(tml + t).x);
+  for (int s = 32 + lane; s < sE; s += 32) M = fmaxf(M, __ldcg(ml + s).x);
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float L = 0.f;
   for (int c0 = 0; c0 < sE; c0 += 32) {
-    float2 r = make_float2(-INFINITY, 0.f);
-    if (c0 + lane < sE) r = __ldcg(ml + c0 + lane);
-    const float w = merge_weight(r.x, M);
-    for (int k0 = 0; k0 < 32 && c0 + k0 < sE; k0 += 8) {
-      Vec v[8];
+    if (c0) r = c0 + lane < sE ? __ldcg(ml + c0 + lane) : none;
+    __syncwarp();
+    weights[warp][lane] = make_float2(merge_weight(r.x, M), r.y);
+    __syncwarp();
+    for (int k0 = 0; k0 < 32 && c0 + k0 < sE; k0 += NB) {
+      Vec x[NB];
+      const int ahead = c0 + k0 + NB;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c0 + k0 + k < sE) v[k] = load(po + (int64_t)(c0 + k0 + k) * HD);
+      for (int k = 0; k < NB; ++k) x[k] = load(po + (int64_t)(ahead + k) * HD, ahead + k < sE);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k0 + k), lk = __shfl_sync(0xffffffffu, r.y, k0 + k);
-        if (c0 + k0 + k < sE) {
-          L = merge_term(L, lk, wk);
+      for (int k = 0; k < NB; ++k) {
+        const float2 wl = weights[warp][k0 + k];
+        L = merge_term(L, wl.y, wl.x);
 #pragma unroll
-          for (int e = 0; e < NE; ++e) O.v[e] = merge_term(O.v[e], v[k].v[e], wk);
-        }
+        for (int e = 0; e < NE; ++e) O.v[e] = merge_term(O.v[e], v[k].v[e], wl.x);
       }
+#pragma unroll
+      for (int k = 0; k < NB; ++k) v[k] = x[k];
     }
   }
   // the split that E cuts, and those behind it
-  Vec P = {};
-  float pm = -INFINITY, pl = 0.f;
-  if (cut) {
-    const float2 r = __ldcg(ml + sE);
-    pm = r.x;
-    pl = r.y;
-    P = load(po + (int64_t)sE * HD);
-  }
-  int t = 0;
-  for (int lb = E; t < n_tail; ++t) {
-    const float2 r = __ldcg(tml + t);
-    const Vec Q = load(to + (int64_t)t * HD);
-    if (r.x != -INFINITY) {
+  float pm = rc.x, pl = rc.y;
+  int lb = E;
+  for (int t = 0; t < n_tail; ++t) {
+    const float2 x = t < 32 ? make_float2(__shfl_sync(0xffffffffu, rt.x, t & 31), __shfl_sync(0xffffffffu, rt.y, t & 31))
+                            : __ldcg(tml + t);
+    if (t > 0) Q = load(to + (int64_t)t * HD, true);
+    if (x.x != -INFINITY) {
       if (pm == -INFINITY) {
-        pm = r.x;
-        pl = r.y;
+        pm = x.x;
+        pl = x.y;
         P = Q;
       } else {
-        const float m = fmaxf(pm, r.x);
+        const float m = fmaxf(pm, x.x);
         const float fa = pm == m ? 1.0f : exp2f(__fsub_rn(pm, m));
-        const float fb = r.x == m ? 1.0f : exp2f(__fsub_rn(r.x, m));
-        pl = __fadd_rn(__fmul_rn(pl, fa), __fmul_rn(r.y, fb));
+        const float fb = x.x == m ? 1.0f : exp2f(__fsub_rn(x.x, m));
+        pl = __fadd_rn(__fmul_rn(pl, fa), __fmul_rn(x.y, fb));
 #pragma unroll
         for (int e = 0; e < NE; ++e) P.v[e] = __fadd_rn(__fmul_rn(P.v[e], fa), __fmul_rn(Q.v[e], fb));
         pm = m;
