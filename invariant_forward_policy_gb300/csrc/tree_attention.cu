@@ -191,7 +191,7 @@ __device__ __forceinline__ void tree_pv(const float (&p)[8][4], int lane, LaneSt
 // row for a position before `start`, the path node's row behind it, a row of zeros behind the node (as a plain decode
 // reads positions behind its own).  8-key groups of scores and 16-key steps of P V behind the node's position are
 // left out.  Most of a 16-row tile is empty for small groups; the chain of one node's few tiles is the time.
-constexpr int kTailWarps = 8;
+constexpr int kTailWarps = 4;
 
 // Shared memory: the page ring; then barriers, depths, parents, the warps' path tables.  The zero row is 128 bytes
 // behind the ring and, for the second half of 128 head dims, 128 bytes 8 KB on: where V would be of a K row kPage
@@ -209,7 +209,7 @@ struct TailLayout {
 };
 
 template <int HD>
-__global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(const TreeArgs a,
+__global__ void __launch_bounds__(kTailWarps * 32, HD == 64 ? 4 : 2) tree_tail_kernel(const TreeArgs a,
                                                                     const __grid_constant__ CUtensorMap tmk,
                                                                     const __grid_constant__ CUtensorMap tmv) {
   using Lay = TailLayout<HD>;
@@ -458,6 +458,24 @@ BI_DEV bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
   return one != 0;
 }
+// Wait for this thread's TMEM loads; r: the registers of one, which nothing may read before.
+template <int N>
+BI_DEV void tmem_ld_wait_for(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 16)  // (the first waits; the others only tie their registers to it)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                   "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
+                   "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15])
+                 :
+                 : "memory");
+}
+// Eight floats, 32-byte aligned.
+BI_DEV void store8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
 // Two products, each rounded once: x y + nz with nz = (-0, -0), a value that the compiler cannot see.  (It contracts
 // mul.rn.f32x2 and a following add.rn.f32x2 into one rounding.)
 BI_DEV float2 mul2(float2 x, float2 y, float nz) {
@@ -693,17 +711,19 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
       int t = 0;        // tiles so far
       bool ok = true;
       int seg = 0;      // row tiles so far
+      // descriptors count addresses in 16 bytes, so one of another address is a sum away
+      const uint64_t q_desc = sw128_kmajor_desc(smem_u32(sQ));
+      const uint64_t k_desc = sw128_kmajor_desc(smem_u32(sKV));
+      const uint64_t v_desc = sw128_mnmajor_desc(smem_u32(sKV), kKeys * 128, 1024);
       auto issue_s = [&](int t) -> bool {
         const int i = 2 * t;
         if (!mbar_wait(&kv_full[i % NS], (i / NS) & 1)) return false;
         tc_fence_after();
-        const uint32_t qa = smem_u32(sQ), ka = smem_u32(sKV + i % NS * Lay::kPage);
+        const uint64_t kd = k_desc + (uint32_t)(i % NS) * (Lay::kPage / 16);
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {
-          const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32, koff = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
-          tc_mma_bf16(tmem + Lay::kColS + (t & 1) * kKeys, sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + koff),
-                      idesc_s, k != 0 ? 1u : 0u);
-        }
+        for (int k = 0; k < HD / 16; ++k)
+          tc_mma_bf16(tmem + Lay::kColS + (t & 1) * kKeys, q_desc + ((k >> 2) * (128 * 128) + (k & 3) * 32) / 16,
+                      kd + ((k >> 2) * (kKeys * 128) + (k & 3) * 32) / 16, idesc_s, k != 0 ? 1u : 0u);
         tc_commit(&s_full[t & 1]);
         tc_commit(&kv_empty[i % NS]);
         return true;
@@ -729,12 +749,11 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
             break;
           }
           tc_fence_after();
-          const uint32_t va = smem_u32(sKV + i % NS * Lay::kPage);
+          const uint64_t vd = v_desc + (uint32_t)(i % NS) * (Lay::kPage / 16);
 #pragma unroll
           for (int x = 0; x < kKeys / 16; ++x)  // a lane's first tile starts from nothing
-            tc_mma_bf16_ts(tmem + Lay::kColO, tmem + Lay::kColS + (t & 1) * kKeys + x * 8,
-                           sw128_mnmajor_desc(va + x * 16 * 128, kKeys * 128, 1024), idesc_o,
-                           x == 0 && i_lane == 0 ? 0u : 1u);
+            tc_mma_bf16_ts(tmem + Lay::kColO, tmem + Lay::kColS + (t & 1) * kKeys + x * 8, vd + x * (16 * 128 / 16),
+                           idesc_o, x == 0 && i_lane == 0 ? 0u : 1u);
           tc_commit(o_done);
           tc_commit(&kv_empty[i % NS]);
           if (++i_lane == tpl) i_lane = 0;
@@ -809,28 +828,30 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
       }
       const bool any_skip = __any_sync(0xffffffffu, skip);
       const float2 fa2 = make_float2(fa, fa), fb2 = make_float2(fb, fb);
+      uint32_t ob[2][16];  // 16 columns at hand and the next on their way
+      tmem_ld_32x32b_x16(tO, ob[0]);
 #pragma unroll
-      for (int c = 0; c < HD; c += 32) {
-        uint32_t o[32];
-        tmem_ld_32x32b_x32(tO + c, o);
-        tmem_ld_wait();
+      for (int c = 0; c < HD; c += 16) {
+        uint32_t(&o)[16] = ob[(c / 16) & 1];
+        tmem_ld_wait_for(o);
+        if (c + 16 < HD) tmem_ld_32x32b_x16(tO + c + 16, ob[(c / 16 + 1) & 1]);
         if (any_skip) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = skip ? 0u : o[k];
+          for (int k = 0; k < 16; ++k) o[k] = skip ? 0u : o[k];
         }
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
+        for (int k = 0; k < 16; k += 2) {
           const float2 z = add2(mul2(make_float2(run[c + k], run[c + k + 1]), fa2, nz),
                                 mul2(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), fb2, nz));
           run[c + k] = z.x;
           run[c + k + 1] = z.y;
         }
         if (s >= 0) {
-          float4* po = reinterpret_cast<float4*>(a.part_o + (rec0 + s) * HD + c);
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            if (rec0 >= 0) po[k / 4] = make_float4(run[c + k], run[c + k + 1], run[c + k + 2], run[c + k + 3]);
-            run[c + k] = run[c + k + 1] = run[c + k + 2] = run[c + k + 3] = 0.f;
+          for (int k = 0; k < 16; k += 8) {
+            if (rec0 >= 0) store8(a.part_o + (rec0 + s) * HD + c + k, run + c + k);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) run[c + k + e] = 0.f;
           }
         }
       }
@@ -860,9 +881,11 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
         if (live) {
           const uint32_t tS = tmem + lane_base + Lay::kColS + (t & 1) * kKeys;
           uint32_t s[64];
-          tmem_ld_32x32b_x32(tS, *reinterpret_cast<uint32_t (*)[32]>(&s[0]));
-          tmem_ld_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t (*)[32]>(&s[32]));
-          tmem_ld_wait();
+          uint32_t(&s_lo)[32] = *reinterpret_cast<uint32_t (*)[32]>(&s[0]);
+          uint32_t(&s_hi)[32] = *reinterpret_cast<uint32_t (*)[32]>(&s[32]);
+          tmem_ld_32x32b_x32(tS, s_lo);
+          tmem_ld_32x32b_x32(tS + 32, s_hi);
+          tmem_ld_wait_for(s);
           // the largest score is the largest product's (scale > 0 and rounding is monotone)
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -908,18 +931,20 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
             fold(lm, ll, i_split == 0 ? split - 1 : -1);
           } else if (live && __any_sync(0xffffffffu, alpha != 1.0f)) {
             const float2 al = make_float2(alpha, alpha);
+            uint32_t ob[2][16];
+            tmem_ld_32x32b_x16(tO, ob[0]);
 #pragma unroll
-            for (int c = 0; c < HD; c += 32) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(tO + c, o);
-              tmem_ld_wait();
+            for (int c = 0; c < HD; c += 16) {
+              uint32_t(&o)[16] = ob[(c / 16) & 1];
+              tmem_ld_wait_for(o);
+              if (c + 16 < HD) tmem_ld_32x32b_x16(tO + c + 16, ob[(c / 16 + 1) & 1]);
 #pragma unroll
-              for (int j = 0; j < 32; j += 2) {
+              for (int j = 0; j < 16; j += 2) {
                 const float2 x = mul2(make_float2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])), al, nz);
                 o[j] = __float_as_uint(x.x);
                 o[j + 1] = __float_as_uint(x.y);
               }
-              tmem_st_32x32b_x32(tO + c, o);
+              tmem_st_32x32b_x16(tO + c, o);
             }
           }
         }
@@ -1130,7 +1155,7 @@ static bi_status launch_tree(TreeArgs args, int64_t B, cudaStream_t st) {
       !encode_tmap_2d_bf16(&tmv, args.v_cache, HD, rows, HD * 2, 64, kKeys, true))
     return fail(BI_ERR_CUDA, "bi_tree_attention: cuTensorMapEncodeTiled failed for the K/V cache");
   // pages that can hold a tile's nodes and their ancestors together with the last context tokens before them
-  args.stages = std::max(HD == 128 ? 3 : 6, (63 + args.max_nodes + 63) / 64);
+  args.stages = std::max(3, (63 + args.max_nodes + 63) / 64);
   const int64_t r = (int64_t)args.max_nodes * args.group;
   const int per_cta = kTailWarps / ((args.group + 15) / 16);  // nodes of a CTA
   BI_TRY(launched(launch_pdl(tree_tail_kernel<HD>,
