@@ -20,16 +20,18 @@ struct TurnRates {
 };
 
 // cos and sin of t * 2^-64 turns, times amp, each within 0.6 units of the last place (amp = 1).
-// r = the offset from the nearest quarter turn, as a sum s + e of two floats (|s| <= pi/4);
-// sin = s + (e (1 - s^2/2) + s^3 P(s^2)), cos = (1 - s^2/2) + (s^4 Q(s^2) - s e) with the roundings of s^2 and
-// of 1 - s^2/2 carried along, P and Q the Taylor series (next terms below 2^-29).
+// The offset from the nearest quarter turn is a sum s + e of two floats (|s| <= pi/4); sin = s + (e (1 - s^2/2) + s^3
+// P(s^2)), cos = (1 - s^2/2) + (s^4 Q(s^2) - s e) with the roundings of s^2 and of 1 - s^2/2 carried along, P and Q the
+// Taylor series (next terms below 2^-29).  The table is bound by its instructions (about 14 on integers, which run at
+// half rate, and 30 on floats a pair) next to its 8 bytes a pair, so the reduction works on the high word: the quarter
+// is its two high bits after adding an eighth of a turn, and its offset converts as 24 bits that a float holds exactly
+// and the 32 bits behind them.
+template <bool AMP>
 BI_DEV void turn_cos_sin(uint64_t t, float amp, float& c_out, float& s_out) {
-  const uint64_t quarter = (t + (1ull << 61)) >> 62;
-  const int64_t r = (int64_t)(t - (quarter << 62));
-  // |r| = a 2^37 + b 2^5 (+ less than 2^5): a fits a float's 24 bits, and of a small angle b holds 24 bits
-  const uint64_t u = (uint64_t)(r < 0 ? -r : r);
-  const float a = (float)(int)(u >> 37) * 0x1p-27f;
-  const float b = (float)(uint32_t)((u & ((1ull << 37) - 1)) >> 5) * 0x1p-59f;
+  const uint32_t hi = (uint32_t)(t >> 32) + 0x20000000u, lo = (uint32_t)t;
+  const int r = (int)(hi & 0x3FFFFFFFu) - 0x20000000;  // the offset's high word, in 2^-32 turns
+  const float a = (float)(r & ~0x3F) * 0x1p-32f;
+  const float b = (float)__funnelshift_l(lo, (uint32_t)r, 26) * 0x1p-58f;
   constexpr float kH = 6.28318548202514648f;   // 2 pi rounded to fp32, and the rest
   constexpr float kL = -1.74845553146951715e-7f;
   const float xh = a * kH;
@@ -45,20 +47,18 @@ BI_DEV void turn_cos_sin(uint64_t t, float amp, float& c_out, float& s_out) {
   const float Q = __fmaf_rn(z, __fmaf_rn(z, __fmaf_rn(z, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f);
   const float st = __fmaf_rn(e, w, s * z * P);
   const float ct = wt + __fmaf_rn(z * z, Q, __fmaf_rn(-s, e, -0.5f * zl));
-  const float sp = __fmaf_rn(amp, s, amp * st);
-  const float sn = r < 0 ? -sp : sp;
-  const float cs = __fmaf_rn(amp, w, amp * ct);
-  const bool odd = quarter & 1;
-  const float c0 = odd ? sn : cs, s0 = odd ? cs : sn;
-  c_out = (quarter + 1) & 2 ? -c0 : c0;
-  s_out = quarter & 2 ? -s0 : s0;
+  const float sn = AMP ? __fmaf_rn(amp, s, amp * st) : s + st;
+  const float cs = AMP ? __fmaf_rn(amp, w, amp * ct) : w + ct;
+  const bool odd = hi & 0x40000000u;
+  c_out = __uint_as_float(__float_as_uint(odd ? sn : cs) ^ ((hi + 0x40000000u) & 0x80000000u));
+  s_out = __uint_as_float(__float_as_uint(odd ? cs : sn) ^ (hi & 0x80000000u));
 }
 
-// A thread holds V neighbouring pairs and walks positions; a block's `rows_step` row groups are neighbours.
-template <int V>
+// A thread holds V neighbouring pairs and walks positions, all CTAs side by side; a CTA's `rows_step` row groups are
+// neighbours.
+template <int V, bool AMP>
 __global__ void __launch_bounds__(256) rope_scaled_table_kernel(float* __restrict__ table, int64_t max_pos, int half,
-                                                                int iters, float amp,
-                                                                const __grid_constant__ TurnRates rates) {
+                                                                float amp, const __grid_constant__ TurnRates rates) {
   pdl_trigger();
   pdl_wait();
   const int nq = half / V;
@@ -66,18 +66,19 @@ __global__ void __launch_bounds__(256) rope_scaled_table_kernel(float* __restric
   const int q = threadIdx.x % nq, r = threadIdx.x / nq;
   if (r >= rows_step) return;
   uint64_t w[V], t[V];
-  int64_t p = (int64_t)blockIdx.x * rows_step * iters + r;
+  int64_t p = (int64_t)blockIdx.x * rows_step + r;
+  const int64_t step = (int64_t)gridDim.x * rows_step;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     w[k] = rates.w[q * V + k];
     t[k] = w[k] * (uint64_t)p;
-    w[k] *= (uint64_t)rows_step;
+    w[k] *= (uint64_t)step;
   }
-  for (int i = 0; i < iters && p < max_pos; ++i, p += rows_step) {
+  for (; p < max_pos; p += step) {
     float c[V], s[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      turn_cos_sin(t[k], amp, c[k], s[k]);
+      turn_cos_sin<AMP>(t[k], amp, c[k], s[k]);
       t[k] += w[k];
     }
     float* row = table + p * (2 * half) + q * V;
@@ -103,8 +104,12 @@ struct SlotWriteArgs {
   __nv_bfloat16* k_cache;
   __nv_bfloat16* v_cache;  // [n_blocks, Hkv, 64, hd]
   int Hq, Hkv, hd, rot;
+  uint32_t per_inv, hv_inv;  // 2^32 / divisor, rounded up (0: divisor 1)
   int* status;
 };
+
+// i / d for i d < 2^32, inv = 2^32 / d rounded up
+BI_DEV int fast_div(int i, uint32_t inv) { return inv ? (int)__umulhi((uint32_t)i, inv) : i; }
 
 // (x1, x2) -> (x1 c - x2 s, x2 c + x1 s), every product and sum rounded, one rounding to bf16: bi_rope_kv_write's
 BI_DEV void rotate_pair(float x1, float x2, float c, float s, float& y1, float& y2) {
@@ -112,9 +117,10 @@ BI_DEV void rotate_pair(float x1, float x2, float c, float s, float& y1, float& 
   y2 = __fadd_rn(__fmul_rn(x2, c), __fmul_rn(x1, s));
 }
 
-// One CTA a row; 16-byte vectors of 8 elements.  The items of a row are, per q and k head, its rotated vectors
-// (half layout: a vector of the first half with its partner; interleaved: a vector of four pairs), then the
-// vectors of its unrotated part, then the vectors of v.
+// One CTA a row; 16-byte vectors of 8 elements.  The items of a row are, per q and k head, its rotated vectors (half
+// layout: a vector of the first half with its partner; interleaved: a vector of four pairs) and the vectors of its
+// unrotated part, then the vectors of v.  Bound by the loads' latency with as many rows in flight as the SMs hold: a
+// thread reads two items before it needs the row's numbers, whose loads run beside them.
 template <bool INTER>
 __global__ void __launch_bounds__(128) rope_slot_write_kernel(const SlotWriteArgs a) {
   pdl_trigger();
@@ -122,72 +128,92 @@ __global__ void __launch_bounds__(128) rope_slot_write_kernel(const SlotWriteArg
   const int64_t row = blockIdx.x;
   const int64_t pos = a.pos[row];
   const int64_t slot = a.slots[row];
+  const uint4* src = reinterpret_cast<const uint4*>(a.qkv + row * a.ld);
+  const int hv = a.hd / 8, half = a.rot / 2;
+  const int nrot = INTER ? a.rot / 8 : a.rot / 16;  // rotated items of a head
+  const int per = hv - a.rot / 8 + nrot;
+  const int n_qk = (a.Hq + a.Hkv) * per, n = n_qk + a.Hkv * hv;
+  struct Item {
+    int h, k;   // head (q, k, then v), vector of it
+    bool turn;  // rotated
+    uint4 x, y; // the vector, and (half layout) its partner
+  };
+  auto read = [&](int i) {
+    Item t;
+    if (i >= n_qk) {
+      t.h = fast_div(i - n_qk, a.hv_inv);
+      t.k = i - n_qk - t.h * hv;
+      t.h += a.Hq + a.Hkv;
+      t.turn = false;
+    } else {
+      t.h = fast_div(i, a.per_inv);
+      t.k = i - t.h * per;
+      t.turn = t.k < nrot;
+      if (!t.turn) t.k += a.rot / 8 - nrot;
+    }
+    t.x = src[t.h * hv + t.k];
+    if (!INTER && t.turn) t.y = src[t.h * hv + t.k + nrot];
+    return t;
+  };
+  const int tid = threadIdx.x;
+  Item one{}, two{};
+  if (tid < n) one = read(tid);
+  if (tid + 128 < n) two = read(tid + 128);
   if (pos < 0 || pos >= a.max_pos) {
-    if (threadIdx.x == 0) report(a.status, DEV_BAD_INDEX);
+    if (tid == 0) report(a.status, DEV_BAD_INDEX);
     return;
   }
   const bool slot_ok = slot >= 0 && slot < a.n_slots;
-  if (!slot_ok && threadIdx.x == 0) report(a.status, DEV_BAD_INDEX);
-  const uint4* src = reinterpret_cast<const uint4*>(a.qkv + row * a.ld);
+  if (!slot_ok && tid == 0) report(a.status, DEV_BAD_INDEX);
   const float* cs = a.table + pos * a.rot;
-  const int hv = a.hd / 8, half = a.rot / 2;
-  const int nrot = INTER ? a.rot / 8 : a.rot / 16;  // rotated items of a head
-  const int rest = hv - a.rot / 8;
-  const int per = nrot + rest;
-  const int n_qk = (a.Hq + a.Hkv) * per;
   uint4* qd = reinterpret_cast<uint4*>(a.q_out) + row * a.Hq * hv;
-  // vector 0 of kv head 0 at this slot, and the distance of the next head
-  const int64_t page = slot >> 6;
-  const int64_t kv0 = (page * a.Hkv * 64 + (slot & 63)) * hv;
-  uint4* kd = reinterpret_cast<uint4*>(a.k_cache) + kv0;
-  uint4* vd = reinterpret_cast<uint4*>(a.v_cache) + kv0;
-  for (int i = threadIdx.x; i < n_qk + a.Hkv * hv; i += blockDim.x) {
-    if (i >= n_qk) {
-      const int j = i - n_qk;
-      if (slot_ok) vd[(int64_t)(j / hv) * 64 * hv + j % hv] = src[(a.Hq + a.Hkv) * hv + j];
-      continue;
+  // vector 0 of kv head 0 at this slot; the next head's is 64 hv further
+  const int64_t kv0 = ((slot >> 6) * a.Hkv * 64 + (slot & 63)) * hv;
+  auto write = [&](const Item& t) {
+    if (t.h >= a.Hq && !slot_ok) return;
+    uint4* y = t.h < a.Hq ? qd + t.h * hv
+               : t.h < a.Hq + a.Hkv
+                   ? reinterpret_cast<uint4*>(a.k_cache) + kv0 + (int64_t)(t.h - a.Hq) * 64 * hv
+                   : reinterpret_cast<uint4*>(a.v_cache) + kv0 + (int64_t)(t.h - a.Hq - a.Hkv) * 64 * hv;
+    if (!t.turn) {
+      y[t.k] = t.x;
+      return;
     }
-    const int h = i / per, k = i % per;
-    if (h >= a.Hq && !slot_ok) continue;
-    const uint4* x = src + h * hv;
-    uint4* y = h < a.Hq ? qd + h * hv : kd + (int64_t)(h - a.Hq) * 64 * hv;
-    if (k >= nrot) {
-      const int j = a.rot / 8 + k - nrot;
-      y[j] = x[j];
-      continue;
-    }
+    const uint32_t w1[4] = {t.x.x, t.x.y, t.x.z, t.x.w};
+    uint32_t o1[4], o2[4];
     if constexpr (INTER) {
-      const uint4 in = x[k];
-      const float4 c = *reinterpret_cast<const float4*>(cs + k * 4);
-      const float4 s = *reinterpret_cast<const float4*>(cs + half + k * 4);
-      const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+      const float4 c = *reinterpret_cast<const float4*>(cs + t.k * 4);
+      const float4 s = *reinterpret_cast<const float4*>(cs + half + t.k * 4);
       const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-      uint32_t o[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float y1, y2;
-        rotate_pair(bf16lo(w[e]), bf16hi(w[e]), cc[e], ss[e], y1, y2);
-        o[e] = pack_bf16x2(y1, y2);
+        rotate_pair(bf16lo(w1[e]), bf16hi(w1[e]), cc[e], ss[e], y1, y2);
+        o1[e] = pack_bf16x2(y1, y2);
       }
-      y[k] = make_uint4(o[0], o[1], o[2], o[3]);
     } else {
-      const uint4 in1 = x[k], in2 = x[k + nrot];
-      const uint32_t w1[4] = {in1.x, in1.y, in1.z, in1.w}, w2[4] = {in2.x, in2.y, in2.z, in2.w};
-      uint32_t o1[4], o2[4];
+      const uint32_t w2[4] = {t.y.x, t.y.y, t.y.z, t.y.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 c = *reinterpret_cast<const float2*>(cs + k * 8 + e * 2);
-        const float2 s = *reinterpret_cast<const float2*>(cs + half + k * 8 + e * 2);
+      for (int e = 0; e < 4; e += 2) {
+        const float4 c = *reinterpret_cast<const float4*>(cs + t.k * 8 + e * 2);
+        const float4 s = *reinterpret_cast<const float4*>(cs + half + t.k * 8 + e * 2);
         float a1, a2, b1, b2;
         rotate_pair(bf16lo(w1[e]), bf16lo(w2[e]), c.x, s.x, a1, b1);
         rotate_pair(bf16hi(w1[e]), bf16hi(w2[e]), c.y, s.y, a2, b2);
         o1[e] = pack_bf16x2(a1, a2);
         o2[e] = pack_bf16x2(b1, b2);
+        rotate_pair(bf16lo(w1[e + 1]), bf16lo(w2[e + 1]), c.z, s.z, a1, b1);
+        rotate_pair(bf16hi(w1[e + 1]), bf16hi(w2[e + 1]), c.w, s.w, a2, b2);
+        o1[e + 1] = pack_bf16x2(a1, a2);
+        o2[e + 1] = pack_bf16x2(b1, b2);
       }
-      y[k] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-      y[k + nrot] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+      y[t.k + nrot] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
     }
-  }
+    y[t.k] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+  };
+  if (tid < n) write(one);
+  if (tid + 128 < n) write(two);
+  for (int i = tid + 256; i < n; i += 128) write(read(i));
 }
 
 // Angle a position of pair i, in turns (64 bits).
@@ -243,12 +269,12 @@ bi_status bi_rope_scaled_table(float* rope_table, int64_t max_pos, int rot, doub
   const int half = rot / 2;
   const bool vec = half % 4 == 0 && aligned16(rope_table);
   const int rows_step = 256 / (half / (vec ? 4 : 1));
-  const int64_t iters = std::min<int64_t>(16, std::max<int64_t>(1, max_pos / ((int64_t)rows_step * 8 * num_sms())));
-  const int64_t blocks = cdiv(max_pos, rows_step * iters);
-  BI_REQUIRE_SHAPE(blocks <= 0x7fffffff, "table too large");
-  auto kernel = vec ? rope_scaled_table_kernel<4> : rope_scaled_table_kernel<1>;
+  const int64_t blocks = std::min<int64_t>(cdiv(max_pos, rows_step), 5 * (int64_t)num_sms());
+  const bool amp = (float)s.amplitude != 1.0f;
+  auto kernel = vec ? (amp ? rope_scaled_table_kernel<4, true> : rope_scaled_table_kernel<4, false>)
+                    : (amp ? rope_scaled_table_kernel<1, true> : rope_scaled_table_kernel<1, false>);
   return launched(launch_pdl(kernel, dim3((unsigned)blocks), dim3(256), 0, as_stream(stream), rope_table, max_pos,
-                             half, (int)iters, (float)s.amplitude, rates),
+                             half, (float)s.amplitude, rates),
                   "bi_rope_scaled_table");
 }
 
@@ -271,9 +297,12 @@ bi_status bi_rope_slot_write(const void* qkv, int64_t T, int64_t ld, const int32
   BI_REQUIRE(aligned16(qkv) && aligned16(q_out) && aligned16(k_cache) && aligned16(v_cache) && aligned16(rope_table),
              "pointers must be 16-byte aligned");
   BI_REQUIRE(T <= 0x7fffffff && n_blocks <= 0x7fffffff, "too many rows or blocks");
+  auto inverse = [](int d) { return d > 1 ? (uint32_t)(((uint64_t(1) << 32) + d - 1) / d) : 0u; };
   SlotWriteArgs a{static_cast<const __nv_bfloat16*>(qkv), ld, row_pos, slots, rope_table, max_pos, n_blocks * 64,
                   static_cast<__nv_bfloat16*>(q_out), static_cast<__nv_bfloat16*>(k_cache),
-                  static_cast<__nv_bfloat16*>(v_cache), Hq, Hkv, hd, rot, device_status_ptr()};
+                  static_cast<__nv_bfloat16*>(v_cache), Hq, Hkv, hd, rot,
+                  inverse(hd / 8 - rot / 8 + rot / (layout == BI_ROPE_HALF ? 16 : 8)), inverse(hd / 8),
+                  device_status_ptr()};
   auto kernel = layout == BI_ROPE_INTERLEAVED ? rope_slot_write_kernel<true> : rope_slot_write_kernel<false>;
   return launched(launch_pdl(kernel, dim3((unsigned)T), dim3(128), 0, as_stream(stream), a), "bi_rope_slot_write");
 }

@@ -92,12 +92,13 @@ constexpr int kAcceptThreads = 256;
 // CTA (x, b): every CTA of a sequence walks its tree (each child that carries the token chosen at its parent
 // bids for it, the lowest index wins; then a chain of at most n shared-memory loads), the first one writes the
 // result, and each moves its share of the accepted rows.  A thread moves one 16-byte vector of every row of the
-// path, in path order.  That order makes the move safe in place: row j goes to start + j, and a later row k > j
-// comes from node path[k] >= k > j, so no row is written over before it is read.
+// path, in path order, four rows read before they are written.  That order makes the move safe in place: row j goes
+// to start + j, and a later row k > j comes from node path[k] >= k > j, so no row is written over before it is read.
+// Bound by the chain of loads (row offsets; tree and block ids; rows): nothing else depends on the walk.
 __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const AcceptArgs a) {
   __shared__ int32_t next[kMaxTreeNodes], target[kMaxTreeNodes];
   __shared__ int32_t path[kMaxTreeNodes];
-  __shared__ int64_t src[kMaxTreeNodes], dst[kMaxTreeNodes];  // slots of the rows that move
+  __shared__ int64_t slot_of[kMaxTreeNodes];  // of cache position start + i, -1 without a block
   __shared__ int count;
   pdl_trigger();
   pdl_wait();
@@ -114,6 +115,11 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const Accep
     tok = a.tokens[r0 + tid];
     target[tid] = a.targets[r0 + tid];
     next[tid] = n;
+    if (a.k) {
+      const int64_t at = start + tid;
+      const int32_t id = at / kPage < a.max_blk ? a.table[(int64_t)b * a.max_blk + at / kPage] : -1;
+      slot_of[tid] = id >= 0 && id < a.n_blocks ? (int64_t)id * kPage + at % kPage : -1;
+    }
   }
   if (tid == 0) count = 0;
   __syncthreads();
@@ -141,21 +147,7 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const Accep
     }
   }
   if (a.k && m > 1) {
-    if (tid < m) {
-      auto slot_of = [&](int64_t at) -> int64_t {
-        if (at / kPage >= a.max_blk) return -1;
-        const int32_t id = a.table[(int64_t)b * a.max_blk + at / kPage];
-        return id >= 0 && id < a.n_blocks ? (int64_t)id * kPage + at % kPage : -1;
-      };
-      if (path[tid] == tid) {
-        src[tid] = dst[tid] = -1;
-      } else {
-        src[tid] = slot_of(start + path[tid]);
-        dst[tid] = slot_of(start + tid);
-        bad |= src[tid] < 0 || dst[tid] < 0;
-      }
-    }
-    __syncthreads();
+    if (tid < m && path[tid] != tid) bad |= slot_of[path[tid]] < 0 || slot_of[tid] < 0;
     const int items = 2 * a.n_layers * a.Hkv * a.hv;
     for (int i = blockIdx.x * kAcceptThreads + tid; i < items; i += gridDim.x * kAcceptThreads) {
       const int vec = i % a.hv;
@@ -163,8 +155,22 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const Accep
       const int lay = i / (a.hv * a.Hkv);
       uint4* cache = (lay >= a.n_layers ? a.v + (lay - a.n_layers) * a.layer_vecs : a.k + lay * a.layer_vecs) + vec;
       auto at = [&](int64_t slot) { return cache + (((slot >> 6) * a.Hkv + head) * kPage + (slot & 63)) * a.hv; };
-      for (int j = 1; j < m; ++j)
-        if (src[j] >= 0 && dst[j] >= 0) *at(dst[j]) = *at(src[j]);
+      for (int j0 = 1; j0 < m; j0 += 4) {
+        uint4 x[4];
+        int64_t to[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = j0 + e;
+          to[e] = -1;
+          if (j < m && path[j] != j && slot_of[path[j]] >= 0 && slot_of[j] >= 0) {
+            to[e] = slot_of[j];
+            x[e] = *at(slot_of[path[j]]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (to[e] >= 0) *at(to[e]) = x[e];
+      }
     }
   }
   if (bad && first) report(a.status, DEV_BAD_INDEX);
