@@ -88,6 +88,27 @@ def recompute_rows(prompt_lens, n_gen: int):
     return cu, np.concatenate(pd), (np.stack(gd) if n_gen > 1 else None), np.stack(td)
 
 
+def draft_nodes(tokens, parents, last: int, room: int, max_nodes: int):
+    """The nodes of a drafted step: the sequence's last token as node 0, then a draft's tokens (parents[i] is the index
+    of an earlier token of the draft, or -1 for one that follows the last token).  Drafts deeper than the `room` tokens
+    that the sequence still takes, and those beyond max_nodes, are left out with what hangs on them.  Returns
+    (tokens, parents) of the nodes."""
+    toks, pars, depth, node = [int(last)], [-1], [0], {-1: 0}
+    if len(tokens) != len(parents):
+        raise ValueError("a draft has as many parents as tokens")
+    for i, (t, p) in enumerate(zip(tokens, parents)):
+        if not -1 <= p < i:
+            raise ValueError(f"draft token {i} has parent {p}: it must stand before it (-1: the last token)")
+        at = node.get(int(p))
+        if at is None or depth[at] + 1 >= room or len(toks) >= max_nodes:
+            continue
+        node[i] = len(toks)
+        toks.append(int(t))
+        pars.append(at)
+        depth.append(depth[at] + 1)
+    return toks, pars
+
+
 @dataclasses.dataclass
 class KVCache:
     k: torch.Tensor
@@ -379,6 +400,119 @@ class Decoder:
             for _ in range(n_steps - 1):
                 one_step()
         return hist_ids.T.contiguous(), hist_lp.T.contiguous()
+
+    def tree_step(self, tokens: torch.Tensor, parent: torch.Tensor, n_nodes: torch.Tensor, start: torch.Tensor,
+                  max_nodes: int, cache: KVCache, block_table: torch.Tensor, max_ctx: int, sampling=None, u=None):
+        """One pass over a packed tree of drafted tokens per sequence (bi_tree_slot_map): the token chosen at every node
+        and its logprob, (ids [T], logprob [T], row0 [B + 1], row_pos [T]) on the device.  The nodes' keys and values
+        stand in the cache at positions start + node.
+
+        Greedy, or with `sampling` (one entry per sequence) drawn with u (fp32 [T], or a function of (row_seq, row_pos)
+        that gives it).  Every node has the bits of a decode step at the end of its path.  bf16 models only."""
+        if self.fp8:
+            raise ValueError("drafted steps are built for bf16 models")
+        if (sampling is None) != (u is None):
+            raise ValueError("sampling and u go together")
+        s, dev = self.shape, self.device
+        T, B, d, hq, hkv, hd = tokens.numel(), n_nodes.numel(), s.d, s.n_heads_q, s.n_heads_kv, s.head_dim
+        mb = block_table.shape[1]
+
+        def buf(*shape, dtype=torch.bfloat16):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        row0, row_seq, row_pos = (buf(n, dtype=torch.int32) for n in (B + 1, T, T))
+        slots = buf(T, dtype=torch.int64)
+        L.bi_tree_slot_map(parent, n_nodes, start, B, max_nodes, block_table, mb, cache.n_blocks, T, row0, row_seq, row_pos,
+                           slots)
+        h, x, tmp, q, ao = buf(T, d), buf(T, d), buf(T, d), buf(T, hq, hd), buf(T, hq * hd)
+        qkv, act = buf(T, (hq + 2 * hkv) * hd), buf(T, s.ffn)
+        ws = buf(L.bi_tree_attention_workspace_size(T, hq, hd, max_ctx, s.kv_split), dtype=torch.uint8)
+        L.bi_embed(tokens, T, self.w["embed"], s.vocab, d, h)
+        L.bi_rmsnorm(h, None, self.layers[0]["attn_norm"], x, T, d, s.eps)
+        norms = [lw["attn_norm"] for lw in self.layers[1:]] + [self.w["final_norm"]]
+        for li, lw in enumerate(self.layers):
+            L.bi_gemm(x, T, d, lw["wqkv"], qkv.shape[1], qkv)
+            L.bi_rope_slot_write(qkv, T, row_pos, slots, hq, hkv, hd, self.rope_table, self.max_pos, cache.n_blocks, q,
+                                 cache.k[li], cache.v[li])
+            L.bi_tree_attention(q, T, parent, row0, start, B, max_nodes, hq, hkv, hd, cache.k[li], cache.v[li], block_table,
+                                mb, cache.n_blocks, max_ctx, s.kv_split, 1.0 / np.sqrt(np.float32(hd)), ws, ao)
+            L.bi_gemm(ao, T, hq * hd, lw["wo"], d, tmp)
+            L.bi_rmsnorm(tmp, h, lw["ffn_norm"], x, T, d, s.eps)
+            L.bi_gemm(x, T, d, lw["w13"], 2 * s.ffn, act, epilogue=L.BI_EPI_SWIGLU)
+            L.bi_gemm(act, T, s.ffn, lw["w2"], d, tmp)
+            L.bi_rmsnorm(tmp, h, norms[li], x, T, d, s.eps)
+        ids, lp = buf(T, dtype=torch.int32), buf(T, dtype=torch.float32)
+        if sampling is not None:
+            logits = buf(T, s.vocab, dtype=torch.float32)
+            L.bi_gemm(x, T, d, self.w["lm_head"], s.vocab, logits, L.BI_DTYPE_FP32)
+            L.bi_sample(logits, T, s.vocab, sampling, u(row_seq, row_pos) if callable(u) else u, ids, lp,
+                        param_row=row_seq)
+        else:
+            n = L.bi_lm_head_logprob_workspace_size(T, s.vocab, d)
+            L.bi_lm_head_logprob(x, T, d, self.w["lm_head"], s.vocab, None, lp, ids, workspace=buf(n, dtype=torch.uint8))
+        return ids, lp, row0, row_pos
+
+    def rollout_drafted(self, prompts, n_gen: int, cache: KVCache, block_table: torch.Tensor, draft, max_nodes=32,
+                        chunk=2048, prefill_max_tokens=8192, sampling=None, uniforms=None):
+        """rollout() with drafted steps: the same (ids, lp), bit for bit, in fewer passes where drafts are right.
+
+        draft(b, tokens) proposes what may follow the tokens (prompt and generated so far, int32 array) of sequence b:
+        (tokens, parents) of a tree as draft_nodes takes it, ([], []) for none.  A pass scores the last token and the draft
+        (at most max_nodes <= 256 nodes) and keeps the path that the model chose itself (bi_tree_accept).  Every
+        sequence needs blocks for its prompt, n_gen - 1 tokens and max_nodes - 1 drafts more."""
+        B, dev, s = len(prompts), self.device, self.shape
+        if (sampling is None) != (uniforms is None):
+            raise ValueError("sampling and uniforms go together")
+        if uniforms is not None and (tuple(uniforms.shape) != (n_gen, B) or uniforms.dtype != torch.float32):
+            raise ValueError(f"uniforms must be fp32 [{n_gen}, {B}]")
+        lens = np.array([len(p) for p in prompts])
+        if lens.min() < 1 or n_gen < 1 or not 1 <= max_nodes <= 256:
+            raise ValueError("every prompt needs a token, n_gen must be positive and max_nodes in [1, 256]")
+        max_ctx = int(lens.max()) + n_gen + max_nodes - 1
+        if -(-(max_ctx - 1) // 64) > block_table.shape[1] or int(lens.max()) + n_gen > self.max_pos:
+            raise ValueError(f"drafted steps of up to {max_ctx - 1} cache positions need more blocks or RoPE rows")
+        if self.fp8:
+            raise ValueError("drafted steps are built for bf16 models")
+        last = np.cumsum(lens) - 1
+        u0 = None
+        if sampling is not None:
+            u0 = torch.zeros(int(lens.sum()), dtype=torch.float32, device=dev)
+            u0[torch.from_numpy(last).to(dev)] = uniforms[0]
+        lp0, sm0, _ = self.prefill(prompts, cache, block_table, logit_from=[n - 1 for n in lens], chunk=chunk,
+                                   max_tokens=prefill_max_tokens, max_ctx=max_ctx, sampling=sampling, u=u0)
+        toks = [list(np.asarray(p, np.int32)) + [int(t)] for p, t in zip(prompts, sm0.cpu().numpy()[last])]
+        lps = [[float(x)] for x in lp0.cpu().numpy()[last]]
+        start = torch.from_numpy(lens.astype(np.int32)).to(dev)
+        lens_dev = start.clone()
+
+        def u_of(row_seq, row_pos):  # the token behind position p of sequence b is generated token p + 1 - len(prompt)
+            seq = row_seq.long()
+            return uniforms[(row_pos - lens_dev[seq]).long() + 1, seq].contiguous()
+
+        def i32(a):
+            return torch.from_numpy(np.asarray(a, np.int32)).to(dev)
+
+        while any(len(g) < n_gen for g in lps):
+            nodes = [draft_nodes(*draft(b, np.asarray(toks[b], np.int32)), toks[b][-1], n_gen - len(lps[b]), max_nodes)
+                     if len(lps[b]) < n_gen else ([], []) for b in range(B)]
+            tokens, parent = (i32(sum((n[k] for n in nodes), [])) for k in (0, 1))
+            T = tokens.numel()
+            most = max(len(n[0]) for n in nodes)
+            ids, lp, row0, _ = self.tree_step(tokens, parent, i32([len(n[0]) for n in nodes]), start, most, cache,
+                                              block_table, max_ctx, sampling, None if sampling is None else u_of)
+            count, after = (torch.empty(B, dtype=torch.int32, device=dev) for _ in range(2))
+            path, out = (torch.empty((B, most), dtype=torch.int32, device=dev) for _ in range(2))
+            L.bi_tree_accept(parent, row0, start, tokens, ids, B, most, T, most, count, path, out, after,
+                             limit=i32([n_gen - len(g) for g in lps]), n_layers=s.n_layers, Hkv=s.n_heads_kv,
+                             hd=s.head_dim, k_cache=cache.k, v_cache=cache.v, block_table=block_table,
+                             max_blocks_per_seq=block_table.shape[1], n_blocks=cache.n_blocks)
+            start = after
+            count, path, out, row0, lp = (t.cpu().numpy() for t in (count, path, out, row0, lp))
+            for b in range(B):
+                toks[b] += [int(t) for t in out[b, :count[b]]]
+                lps[b] += [float(x) for x in lp[row0[b] + path[b, :count[b]]]]
+        ids = np.stack([np.asarray(t[n:], np.int32) for t, n in zip(toks, lens)])
+        return torch.from_numpy(ids).to(dev), torch.tensor(lps, dtype=torch.float32, device=dev)
 
     def recompute(self, prompts, gens, cache: KVCache, block_table: torch.Tensor, chunk=2048, order=None,
                   mode=L.BI_INVARIANT, max_tokens=8192, max_logit_rows=2048, sampling=None):
