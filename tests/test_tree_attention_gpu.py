@@ -43,6 +43,19 @@ def test_every_split_size(split, n):
     assert same_bits(c.run(split=split), c.linear(split=split))
 
 
+@pytest.mark.parametrize("B,most,hq,hkv,hd,n", [(300, 900, 4, 2, 64, 3), (24, 3500, 8, 2, 128, 9), (3, 9000, 16, 4, 128, 40)])
+def test_many_and_long_sequences(B, most, hq, hkv, hd, n):
+    """More sequences than threads of a CTA, runs of units over several row tiles and sequences, empty ones among them."""
+    rng = np.random.default_rng(B)
+    starts = [int(s) for s in rng.integers(0, most, B)]
+    trees = [make_tree(("levels", "chain", "forest")[b % 3], 0 if b % 7 == 3 else int(rng.integers(1, n + 1)), rng)
+             for b in range(B)]
+    trees[0] = make_tree("levels", n, rng)
+    c = Case(trees, starts, hq, hkv, hd, seed=B, qscale=2.0)
+    assert same_bits(c.run(), c.linear())
+    assert bi.bi_device_status() == bi.BI_OK
+
+
 @pytest.mark.parametrize("hq,hkv,hd,n,qscale", [(8, 8, 64, 16, 1.0), (16, 4, 128, 12, 3.0), (8, 2, 128, 33, 1.0)])
 def test_against_the_oracle(hq, hkv, hd, n, qscale):
     rng = np.random.default_rng(3)
