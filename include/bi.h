@@ -352,7 +352,7 @@ bi_status bi_tree_slot_map(const int32_t* parent, const int32_t* n_nodes, const 
  * bf16 [T, Hq * hd]; caches, block_table (row b for sequence b), kv_split and scale
  * as in bi_attention, kv_split <= 16384, scale > 0; hd in {64, 128}, 64 % (Hq/Hkv) == 0.
  * max_ctx bounds start + depth + 1.  workspace: bi_tree_attention_workspace_size
- * bytes.  Rows of an invalid node, of one beyond max_ctx's last split, and of a
+ * bytes (16-byte aligned as the other pointers; nothing is kept in it).  Rows of an invalid node, of one beyond max_ctx's last split, and of a
  * sequence whose start is below 0 or whose nodes go past its block table are
  * zeros and set the device status; a sequence with more than max_nodes nodes or
  * with rows outside [0, T) writes nothing and sets it; a block id outside

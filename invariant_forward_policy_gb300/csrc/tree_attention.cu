@@ -7,7 +7,6 @@
 // that holds just that path (splits, lanes, 64-key tiles and 16-key MMA steps by position), so it has the bits
 // that a plain decode of the path gives.
 //
-//
 // Three launches.  Let E be the start of the lane (of bi_attention's partition) that holds position `start`.
 //   * tree_tail_kernel: the lanes from E on, which differ by node, on mma.sync; a record (m, l, acc) for each row
 //     and lane.
@@ -16,7 +15,10 @@
 //   * tree_merge_kernel: folds and merges a row's records in order.
 // What bounds it: a page of keys and values is read once for up to 128 query rows (nodes x q heads of a group), so
 // HBM bounds small trees; with more rows the softmax's instructions and the split records (one for every 512
-// positions of every row: as many bytes as the keys and values themselves at 256 rows) do.
+// positions of every row: as many bytes as the keys and values themselves at 256 rows) do.  Measured (GB300, 16 q heads on
+// 4 kv heads of 128, us a call): 64 chains of up to 8 nodes, contexts of 1K to 32K, 228 (1.21 GB at 5.3 TB/s); 16 trees of
+// 64 nodes, contexts of 6K to 8K, 155 (0.24 GB, 58.7 GFLOP); one tree of 37 nodes behind 32K positions 48; 16 trees of 16
+// nodes, contexts up to 768, 8 heads of 64: 25.
 #include <algorithm>
 #include <mutex>
 #include <string>
@@ -45,7 +47,7 @@ struct TreeArgs {
   float neg_zero;  // -0, see mul2
 };
 
-constexpr int kTreeMaxSplit = 16384;  // positions of a split: 256 pages, whose ids stand in shared memory
+constexpr int kTreeMaxSplit = 16384;  // positions of a split (positions near max_ctx stay 32-bit numbers)
 
 // A sequence as the kernels see it: its rows, or none when its numbers cannot be right.
 struct TreeSeq {
@@ -190,7 +192,9 @@ __device__ __forceinline__ void tree_pv(const float (&p)[8][4], int lane, LaneSt
 // an address for every key row, so a tile behind `start` is read as if the node's path stood in the cache: the page's
 // row for a position before `start`, the path node's row behind it, a row of zeros behind the node (as a plain decode
 // reads positions behind its own).  8-key groups of scores and 16-key steps of P V behind the node's position are
-// left out.  Most of a 16-row tile is empty for small groups; the chain of one node's few tiles is the time.
+// left out.  Most of a 16-row tile is empty for small groups; the chain of one node's few tiles is the time (16 x 64
+// nodes x 4 kv heads: 26 us, of which 7 beside the context kernel; a warp of four nodes that selects each node's results
+// from its own MMAs took 51).
 constexpr int kTailWarps = 4;
 
 // Shared memory: the page ring; then barriers, depths, parents, the warps' path tables.  The zero row is 128 bytes
@@ -419,8 +423,13 @@ __global__ void __launch_bounds__(kTailWarps * 32, HD == 64 ? 4 : 2) tree_tail_k
 // keys 8j + 2q + {0, 1}, then (s0 + s1) + (s2 + s3).  Products and sums go two at a time (f32x2: the same
 // roundings).  S of a tile is computed while the one before it is in the softmax, and the accumulator of a finished
 // lane is folded while the next lane's first scores are.
-// Two CTAs share an SM (their chains softmax -> P V -> fold interleave): 114 KB of shared memory and 256 TMEM
-// columns each, and 128 registers a thread at launch, which the warpgroups then split 224 to 32.
+// Two CTAs share an SM (their chains softmax -> P V -> fold interleave): 113 KB of shared memory and 256 TMEM
+// columns each, and 128 registers a thread at launch, which the warpgroups then split 224 to 32.  At 128 live rows a
+// CTA takes 3400 clocks a tile: S 570 to wait for, scores 180, exponentials 720, P V 240 to wait for, fold 1900 a lane,
+// scaling 530 a lane, a record 2000 a split; with two warps a scheduler the chains' latency is what bounds it (issue
+// 41%, tensor pipe 27%).  One row tile's pages twice from memory (a second tile of 128 rows) is the rest: 422 MB read
+// for 236.  Tried and slower: P in shared memory, more O columns a wait (both spill), row tiles in turn for every split
+// (Q changes too often), one CTA an SM with warps of their own for scaling and folds (the fold's chain bounds it).
 template <int HD>
 struct CtxLayout {
   static constexpr int kQ = 128 * HD * 2;       // HD/64 boxes of 128 rows x 128 bytes
@@ -1213,7 +1222,9 @@ bi_status bi_tree_attention(const void* q, int64_t T, const int32_t* parent, con
   const int lane_len = split_lane_len(kv_split);
   const int nt = tail_records(max_nodes, kv_split, lane_len);
   const size_t per = (size_t)T * Hq * ns, per_t = (size_t)T * Hq * nt;
-  BI_REQUIRE(ws_bytes >= (per + per_t) * (hd + 2) * sizeof(float) + (size_t)T * sizeof(int32_t),
+  // records are written 32 bytes at a time
+  const size_t skip = (32 - (reinterpret_cast<uintptr_t>(workspace) & 31)) & 31;
+  BI_REQUIRE(ws_bytes >= skip + (per + per_t) * (hd + 2) * sizeof(float) + (size_t)T * sizeof(int32_t),
              "workspace too small (bi_tree_attention_workspace_size)");
   TreeArgs a;
   a.q = static_cast<const __nv_bfloat16*>(q);
@@ -1221,7 +1232,7 @@ bi_status bi_tree_attention(const void* q, int64_t T, const int32_t* parent, con
   a.row0 = row0;
   a.start = start;
   a.block_table = block_table;
-  a.part_o = static_cast<float*>(workspace);
+  a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + skip);
   a.tail_o = a.part_o + per * hd;
   a.part_ml = a.tail_o + per_t * hd;
   a.tail_ml = a.part_ml + per * 2;

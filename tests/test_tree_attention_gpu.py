@@ -199,6 +199,17 @@ def test_captured_on_another_stream_and_replayed():
     assert same_bits(out, other.run())
 
 
+def test_a_workspace_sixteen_bytes_off():
+    c = Case([make_tree("levels", 12, np.random.default_rng(1))] * 2, [600, 1100], 8, 2, 128, seed=8)
+    k, v = c.caches()
+    q, out = torch.from_numpy(c.q).cuda().to(torch.bfloat16), torch.zeros((c.T, 1024), dtype=torch.bfloat16, device="cuda")
+    n = bi.bi_tree_attention_workspace_size(c.T, 8, 128, c.max_ctx, 512)
+    ws = torch.empty(n + 16, dtype=torch.uint8, device="cuda")[16:]
+    bi.bi_tree_attention(q, c.T, i32(np.concatenate(c.trees)), i32(c.row0), i32(c.starts), c.B, c.max_nodes, 8, 2, 128, k, v,
+                         i32(c.table), c.mb, c.nb, c.max_ctx, 512, c.scale, ws, out)
+    assert same_bits(out, c.run())
+
+
 def test_two_calls_at_once_on_two_streams():
     rng = np.random.default_rng(2)
     cs = [Case([make_tree("levels", 20, rng)] * 4, [900, 64, 1500, 7], 8, 2, 128, seed=s) for s in (1, 2)]
