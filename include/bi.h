@@ -352,12 +352,13 @@ bi_status bi_tree_slot_map(const int32_t* parent, const int32_t* n_nodes, const 
  * bf16 [T, Hq * hd]; caches, block_table (row b for sequence b), kv_split and scale
  * as in bi_attention, kv_split <= 16384, scale > 0; hd in {64, 128}, 64 % (Hq/Hkv) == 0.
  * max_ctx bounds start + depth + 1.  workspace: bi_tree_attention_workspace_size
- * bytes (16-byte aligned as the other pointers; nothing is kept in it).  Rows of an invalid node, of one beyond max_ctx's last split, and of a
- * sequence whose start is below 0 or whose nodes go past its block table are
- * zeros and set the device status; a sequence with more than max_nodes nodes or
- * with rows outside [0, T) writes nothing and sets it; a block id outside
- * [0, n_blocks) reads as zeros and sets it.  Rows behind the last sequence's stay
- * as they were.  One schedule (no mode argument). */
+ * bytes (16-byte aligned as the other pointers; nothing is kept in it).  Rows of
+ * an invalid node, of one beyond max_ctx's last split, and of a sequence whose
+ * start is below 0 or whose nodes go past its block table are zeros and set the
+ * device status; a sequence with more than max_nodes nodes or with rows outside
+ * [0, T) writes nothing and sets it; a block id outside [0, n_blocks) reads as
+ * zeros and sets it.  Rows behind the last sequence's stay as they were.  One
+ * schedule (no mode argument). */
 bi_status bi_tree_attention(const void* q, int64_t T, const int32_t* parent, const int32_t* row0, const int32_t* start,
                             int64_t B, int64_t max_nodes, int Hq, int Hkv, int hd, const void* k_cache,
                             const void* v_cache, const int32_t* block_table, int64_t max_blocks_per_seq,

@@ -405,7 +405,8 @@ class Decoder:
                   max_nodes: int, cache: KVCache, block_table: torch.Tensor, max_ctx: int, sampling=None, u=None):
         """One pass over a packed tree of drafted tokens per sequence (bi_tree_slot_map): the token chosen at every node
         and its logprob, (ids [T], logprob [T], row0 [B + 1], row_pos [T]) on the device.  The nodes' keys and values
-        stand in the cache at positions start + node.
+        stand in the cache at positions start + node.  Rows behind the last sequence's nodes write nothing to the cache and
+        set the device status (so does a sequence with more than max_nodes nodes); their ids and logprobs mean nothing.
 
         Greedy, or with `sampling` (one entry per sequence) drawn with u (fp32 [T], or a function of (row_seq, row_pos)
         that gives it).  Every node has the bits of a decode step at the end of its path.  bf16 models only."""
@@ -415,13 +416,21 @@ class Decoder:
             raise ValueError("sampling and u go together")
         s, dev = self.shape, self.device
         T, B, d, hq, hkv, hd = tokens.numel(), n_nodes.numel(), s.d, s.n_heads_q, s.n_heads_kv, s.head_dim
+        for name, t, n in (("tokens", tokens, T), ("parent", parent, T), ("n_nodes", n_nodes, B), ("start", start, B),
+                           ("block_table", block_table, max(B, block_table.shape[0]) * block_table.shape[1])):
+            if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous int32 with a row per node or sequence")
+        if isinstance(u, torch.Tensor) and (u.dtype != torch.float32 or u.numel() != T or not u.is_contiguous()):
+            raise ValueError("u must be contiguous fp32 with an entry per node")
         mb = block_table.shape[1]
 
         def buf(*shape, dtype=torch.bfloat16):
             return torch.empty(shape, dtype=dtype, device=dev)
 
-        row0, row_seq, row_pos = (buf(n, dtype=torch.int32) for n in (B + 1, T, T))
-        slots = buf(T, dtype=torch.int64)
+        # rows that no sequence owns keep position and slot -1: nothing of theirs reaches the cache
+        row0, row_seq = (torch.zeros(n, dtype=torch.int32, device=dev) for n in (B + 1, T))
+        row_pos = torch.full((T,), -1, dtype=torch.int32, device=dev)
+        slots = torch.full((T,), -1, dtype=torch.int64, device=dev)
         L.bi_tree_slot_map(parent, n_nodes, start, B, max_nodes, block_table, mb, cache.n_blocks, T, row0, row_seq, row_pos,
                            slots)
         h, x, tmp, q, ao = buf(T, d), buf(T, d), buf(T, d), buf(T, hq, hd), buf(T, hq * hd)

@@ -88,3 +88,56 @@ def test_drafted_rollout_refusals():
         dec.rollout_drafted(prompts, 8, cache, bt, lambda b, t: ([1], [0]))
     with pytest.raises(ValueError):
         Decoder(shape, w, max_pos=128, fp8=True).rollout_drafted(prompts, 8, cache, bt, none)
+
+
+def _step_case(n_nodes, extra, seed=81):
+    shape = DecoderShape(2, 128, 4, 2, 64, 256, 512)
+    dec = Decoder(shape, make_decoder_weights(shape, seed=71, w_std=0.05), max_pos=256)
+    rng = np.random.default_rng(seed)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    parent = [int(rng.integers(0, i)) if i else -1 for n in n_nodes for i in range(n)] + [-1] * extra
+    tokens = rng.integers(0, shape.vocab, len(parent)).tolist()
+    cache = dec.alloc_cache(2 * len(n_nodes))
+    for c in (cache.k, cache.v):
+        c.copy_(torch.randn(c.shape, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda"))
+    return dec, i32(tokens), i32(parent), i32(n_nodes), i32([70] * len(n_nodes)), cache, dec.block_table(
+        len(n_nodes), 2, seed=4)
+
+
+def test_tree_step_rows_without_a_sequence_write_nothing():
+    n_nodes, extra = [5, 0, 9], 6
+    dec, tokens, parent, n, start, cache, bt = _step_case(n_nodes, extra)
+    T = sum(n_nodes)
+    before = cache.k.clone(), cache.v.clone()
+    ids, lp, row0, pos = dec.tree_step(tokens[:T].clone(), parent[:T].clone(), n, start, 16, cache, bt, 100)
+    assert bi.bi_device_status() == bi.BI_OK
+    after = cache.k.clone(), cache.v.clone()
+    cache.k.copy_(before[0])
+    cache.v.copy_(before[1])
+    # what the allocator hands out next holds valid slots and positions
+    junk = [torch.full((T + extra,), 7, dtype=t, device="cuda") for t in (torch.int64, torch.int32) for _ in range(8)]
+    del junk
+    ids2, lp2, row02, pos2 = dec.tree_step(tokens, parent, n, start, 16, cache, bt, 100)
+    assert bi.bi_device_status() != bi.BI_OK
+    assert torch.equal(ids2[:T], ids) and same_bits(lp2[:T], lp) and torch.equal(row02, row0)
+    assert torch.equal(pos2[:T], pos) and (pos2[T:] == -1).all()
+    assert same_bits(cache.k, after[0]) and same_bits(cache.v, after[1])
+
+
+def test_tree_step_without_nodes():
+    dec, tokens, parent, n, start, cache, bt = _step_case([0, 0], 0)
+    before = cache.k.clone()
+    ids, lp, row0, pos = dec.tree_step(tokens, parent, n, start, 4, cache, bt, 100)
+    assert ids.numel() == lp.numel() == pos.numel() == 0 and row0.tolist() == [0, 0, 0]
+    assert same_bits(cache.k, before) and bi.bi_device_status() == bi.BI_OK
+
+
+def test_tree_step_refusals():
+    dec, tokens, parent, n, start, cache, bt = _step_case([5, 4], 0)
+    ok = dict(tokens=tokens, parent=parent, n_nodes=n, start=start, max_nodes=8, cache=cache, block_table=bt, max_ctx=100)
+    for bad in (dict(parent=parent[:-1]), dict(tokens=tokens.long()), dict(start=start[:1]), dict(block_table=bt[:1]),
+                dict(parent=torch.stack([parent, parent], 1)[:, 0]), dict(block_table=torch.cat([bt, bt], 1)[:, :2]),
+                dict(sampling=bi.bi_sampling(None, None, None)),
+                dict(sampling=bi.bi_sampling(None, None, None), u=torch.zeros(8, device="cuda"))):
+        with pytest.raises(ValueError):
+            dec.tree_step(**{**ok, **bad})
