@@ -263,6 +263,7 @@ bi_status bi_rope_scaled_table(float* rope_table, int64_t max_pos, int rot, doub
   TurnRates rates = {};
   for (int i = 0; i < rot / 2; ++i) {
     double w = turns_a_position(i, rot, theta, s);
+    BI_REQUIRE(std::isfinite(w), "the scaled angles must be finite");
     w -= floor(w);
     rates.w[i] = w < 1 ? (uint64_t)ldexp(w, 64) : 0;
   }

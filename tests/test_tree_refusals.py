@@ -33,6 +33,8 @@ def test_rope_scaled_table(lib):
                 dict(kind=bi.BI_ROPE_DIMS, factor=2.0, orig_len=0.0), dict(kind=bi.BI_ROPE_DIMS, factor=2.0, high=math.inf)):
         assert call(**bad) == INVALID, bad
     assert call(rot=258) == SHAPE
+    for kind in (bi.BI_ROPE_LINEAR, bi.BI_ROPE_TURNS, bi.BI_ROPE_DIMS):      # angles beyond the range of doubles
+        assert call(kind=kind, factor=5e-324) == INVALID and "finite" in bi.bi_last_error()
 
 
 def test_rope_slot_write(lib):
