@@ -515,7 +515,7 @@ struct CtxCursor {
     b = b_;
     sq = tree_seq(a, b);
     const int E = sq.ok ? tail_lane(a, sq.start) : 0;
-    n_split = min((E + a.split - 1) / a.split, a.nsplit);
+    n_split = min(E / a.split + (E % a.split != 0), a.nsplit);  // (E may be near 2^31)
     n_tile = ((sq.n << a.gshift) + 127) >> 7;
     return (int64_t)n_split * n_tile * a.Hkv;
   }

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import invariant_forward_policy_gb300 as bi
-from gpu_util import host_f32, same_bits
+from gpu_util import dev_bf16_from_f32, host_f32, same_bits
 from oracle import tree
 from tree_util import Case, i32, make_tree
 
@@ -223,3 +223,20 @@ def test_two_calls_at_once_on_two_streams():
     torch.cuda.synchronize()
     for s, o in zip(state, outs):
         assert same_bits(o, s[2])
+
+
+def test_a_start_near_the_end_of_the_widest_table():
+    c = Case([make_tree("levels", 6, np.random.default_rng(1)), [-1, 0, 0]], [600, 8], 8, 2, 128, seed=8)
+    good = c.run()
+    k, v = c.caches()
+    mb = 0x7fffffff // 64
+    table = torch.zeros((2, mb), dtype=torch.int32, device="cuda")
+    table[:, :c.mb] = i32(c.table)
+    table[1, c.mb:] = int(c.table[1, 0])
+    table[1, :c.mb] = int(c.table[1, 0])
+    out = torch.full_like(good, 7.0)
+    ws = torch.empty(bi.bi_tree_attention_workspace_size(c.T, 8, 128, c.max_ctx, 512), dtype=torch.uint8, device="cuda")
+    bi.bi_tree_attention(dev_bf16_from_f32(c.q), c.T, i32(np.concatenate(c.trees)), i32(c.row0), i32([600, mb * 64 - 64]), 2,
+                         c.max_nodes, 8, 2, 128, k, v, table, mb, c.nb, c.max_ctx, 512, c.scale, ws, out)
+    assert bi.bi_device_status() == bi.BI_ERR_DEVICE_CHECK       # beyond max_ctx: zeros
+    assert same_bits(out[:6], good[:6]) and (out[6:] == 0).all()
