@@ -141,3 +141,24 @@ def test_tree_step_refusals():
                 dict(sampling=bi.bi_sampling(None, None, None), u=torch.zeros(8, device="cuda"))):
         with pytest.raises(ValueError):
             dec.tree_step(**{**ok, **bad})
+
+
+def test_tree_step_captured_and_replayed():
+    dec, tokens, parent, n, start, cache, bt = _step_case([5, 0, 9], 0)
+    before = cache.k.clone(), cache.v.clone()
+    other = (tokens + 17) % dec.shape.vocab
+    want = dec.tree_step(other, parent, n, start, 16, cache, bt, 100)
+    end = cache.k.clone(), cache.v.clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = dec.tree_step(tokens, parent, n, start, 16, cache, bt, 100)
+    tokens.copy_(other)
+    for _ in range(2):
+        cache.k.copy_(before[0])
+        cache.v.copy_(before[1])
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and same_bits(got[1], want[1])
+        assert same_bits(cache.k, end[0]) and same_bits(cache.v, end[1])
+    assert bi.bi_device_status() == bi.BI_OK
