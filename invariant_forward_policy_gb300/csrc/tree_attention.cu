@@ -16,8 +16,8 @@
 // What bounds it: a page of keys and values is read once for up to 128 query rows (nodes x q heads of a group), so
 // HBM bounds small trees; with more rows the softmax's instructions and the split records (one for every 512
 // positions of every row: as many bytes as the keys and values themselves at 256 rows) do.  Measured (GB300, 16 q heads on
-// 4 kv heads of 128, us a call): 64 chains of up to 8 nodes, contexts of 1K to 32K, 228 (1.21 GB at 5.3 TB/s); 16 trees of
-// 64 nodes, contexts of 6K to 8K, 155 (0.24 GB, 58.7 GFLOP); one tree of 37 nodes behind 32K positions 48; 16 trees of 16
+// 4 kv heads of 128, us a call): 64 chains of up to 8 nodes, contexts of 1K to 32K, 229 (1.21 GB at 5.3 TB/s); 16 trees of
+// 64 nodes, contexts of 6K to 8K, 150 (0.24 GB, 58.7 GFLOP); one tree of 37 nodes behind 32K positions 46; 16 trees of 16
 // nodes, contexts up to 768, 8 heads of 64: 25.
 #include <algorithm>
 #include <mutex>
@@ -997,14 +997,15 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
 // A warp a (node, q head), HD / 32 neighbouring elements a lane.  The splits before E are merged as the attention merge
 // does (a weight a lane, 32 at a time; sums in ascending order; places behind the last split add 0 * 0, and the sums,
 // which start from +0, are never -0); the split that E cuts and those behind it are first folded from their lanes with
-// lane_merge's formula.  Loads that do not depend on the row's position go out at once, and the next 8 records while
-// 8 are added up.
+// lane_merge's formula.  Loads that do not depend on the row's position go out at once, and the next NB records while
+// NB are added up.  Few rows wait for their records' latency and want many in flight, many rows want the registers for
+// more warps: NB = 16, 8, 4 take 45.9, 47.6, 50.5 us a whole call for 592 rows of 64 splits, 24.6, 25.0, 25.1 for 2048
+// of one, and 168, 153.5, 150.5 for 16384 of 14.
 constexpr int kTreeMergeWarps = 4;
-constexpr int kTreeMergeBatch = 8;
 
-template <int HD>
+template <int HD, int NB>
 __global__ void __launch_bounds__(kTreeMergeWarps * 32) tree_merge_kernel(const TreeArgs a) {
-  constexpr int NE = HD / 32, NB = kTreeMergeBatch;
+  constexpr int NE = HD / 32;
   __shared__ float2 weights[kTreeMergeWarps][32];  // (weight, l) of 32 splits
   pdl_trigger();
   pdl_wait();
@@ -1176,7 +1177,8 @@ static bi_status launch_tree(TreeArgs args, int64_t B, cudaStream_t st) {
   BI_TRY(launched(launch_pdl(tree_context_kernel<HD>, dim3((unsigned)std::min<int64_t>(units, 2 * (int64_t)num_sms())),
                              dim3(Ctx::kThreads), Ctx::kBytes, st, args, tmk, tmv),
                   "tree_context_kernel"));
-  return launched(launch_pdl(tree_merge_kernel<HD>,
+  const bool few = args.T * args.Hq <= 16 * (int64_t)num_sms();
+  return launched(launch_pdl(few ? tree_merge_kernel<HD, 16> : tree_merge_kernel<HD, 4>,
                              dim3((unsigned)args.max_nodes, (unsigned)B, (unsigned)cdiv(args.Hq, kTreeMergeWarps)),
                              dim3(kTreeMergeWarps * 32), 0, st, args),
                   "tree_merge_kernel");
