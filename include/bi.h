@@ -172,10 +172,11 @@ bi_status bi_rope_table(float* rope_table, int64_t max_pos, int hd, double theta
  *   BI_ROPE_DIMS   w_i (1 - r + r / factor), r rising from 0 to 1 over the pairs
  *                  i = floor(d(high)) .. ceil(d(low)) (kept within 0 .. rot - 1),
  *                  d(t) = rot ln(orig_len / (2 pi t)) / (2 ln theta)
- * A NULL scaling is BI_ROPE_PLAIN with amplitude 1.  Entries are within 0.6 units
- * in the last place of |A|, or an angle error of p 2^-52 w_i where that is more,
- * and within one unit of bi_rope_table's (not always its bits).  A decoder uses
- * such a table when its caller overwrites bi_weights.rope_table after
+ * A NULL scaling is BI_ROPE_PLAIN with amplitude 1.  Entries are within |A| (0.6 *
+ * 2^-23 + p 2^-52 w_i) + 2^-148 of the formula (the second part is the angle's own
+ * error; A need not be an fp32 number), plain ones within one unit in the last
+ * place of 1 of bi_rope_table's (not always its bits).  A decoder uses such a table
+ * when its caller overwrites bi_weights.rope_table after
  * bi_model_create.  rot even, 2 <= rot <= 256; theta > 1; max_pos <= 2^31. */
 typedef enum {
   BI_ROPE_PLAIN = 0,

@@ -19,7 +19,8 @@ struct TurnRates {
   uint64_t w[kMaxRot / 2];
 };
 
-// cos and sin of t * 2^-64 turns, times amp, each within 0.6 units of the last place (amp = 1).
+// cos and sin of t * 2^-64 turns, times the amplitude amp (1 + rho) (a 64-bit number; one float alone may be half a unit
+// away), each within 0.6 * 2^-23 of the amplitude.
 // The offset from the nearest quarter turn is a sum s + e of two floats (|s| <= pi/4); sin = s + (e (1 - s^2/2) + s^3
 // P(s^2)), cos = (1 - s^2/2) + (s^4 Q(s^2) - s e) with the roundings of s^2 and of 1 - s^2/2 carried along, P and Q the
 // Taylor series (next terms below 2^-29).  The table is bound by its instructions (about 14 on integers, which run at
@@ -27,7 +28,7 @@ struct TurnRates {
 // is its two high bits after adding an eighth of a turn, and its offset converts as 24 bits that a float holds exactly
 // and the 32 bits behind them.
 template <bool AMP>
-BI_DEV void turn_cos_sin(uint64_t t, float amp, float& c_out, float& s_out) {
+BI_DEV void turn_cos_sin(uint64_t t, float amp, float rho, float& c_out, float& s_out) {
   const uint32_t hi = (uint32_t)(t >> 32) + 0x20000000u, lo = (uint32_t)t;
   const int r = (int)(hi & 0x3FFFFFFFu) - 0x20000000;  // the offset's high word, in 2^-32 turns
   const float a = (float)(r & ~0x3F) * 0x1p-32f;
@@ -45,8 +46,8 @@ BI_DEV void turn_cos_sin(uint64_t t, float amp, float& c_out, float& s_out) {
   const float wt = (1.0f - w) + h;
   const float P = __fmaf_rn(z, __fmaf_rn(z, __fmaf_rn(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f);
   const float Q = __fmaf_rn(z, __fmaf_rn(z, __fmaf_rn(z, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f);
-  const float st = __fmaf_rn(e, w, s * z * P);
-  const float ct = wt + __fmaf_rn(z * z, Q, __fmaf_rn(-s, e, -0.5f * zl));
+  const float st = __fmaf_rn(e, w, AMP ? s * __fmaf_rn(z, P, rho) : s * z * P);
+  const float ct = (AMP ? __fmaf_rn(rho, w, wt) : wt) + __fmaf_rn(z * z, Q, __fmaf_rn(-s, e, -0.5f * zl));
   const float sn = AMP ? __fmaf_rn(amp, s, amp * st) : s + st;
   const float cs = AMP ? __fmaf_rn(amp, w, amp * ct) : w + ct;
   const bool odd = hi & 0x40000000u;
@@ -58,7 +59,8 @@ BI_DEV void turn_cos_sin(uint64_t t, float amp, float& c_out, float& s_out) {
 // neighbours.
 template <int V, bool AMP>
 __global__ void __launch_bounds__(256) rope_scaled_table_kernel(float* __restrict__ table, int64_t max_pos, int half,
-                                                                float amp, const __grid_constant__ TurnRates rates) {
+                                                                float amp, float rho,
+                                                                const __grid_constant__ TurnRates rates) {
   pdl_trigger();
   pdl_wait();
   const int nq = half / V;
@@ -78,7 +80,7 @@ __global__ void __launch_bounds__(256) rope_scaled_table_kernel(float* __restric
     float c[V], s[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      turn_cos_sin<AMP>(t[k], amp, c[k], s[k]);
+      turn_cos_sin<AMP>(t[k], amp, rho, c[k], s[k]);
       t[k] += w[k];
     }
     float* row = table + p * (2 * half) + q * V;
@@ -271,11 +273,13 @@ bi_status bi_rope_scaled_table(float* rope_table, int64_t max_pos, int rot, doub
   const bool vec = half % 4 == 0 && aligned16(rope_table);
   const int rows_step = 256 / (half / (vec ? 4 : 1));
   const int64_t blocks = std::min<int64_t>(cdiv(max_pos, rows_step), 5 * (int64_t)num_sms());
-  const bool amp = (float)s.amplitude != 1.0f;
+  const bool amp = s.amplitude != 1.0;
+  const float near = (float)s.amplitude;
+  const float rho = near != 0 ? (float)((s.amplitude - (double)near) / (double)near) : 0.f;
   auto kernel = vec ? (amp ? rope_scaled_table_kernel<4, true> : rope_scaled_table_kernel<4, false>)
                     : (amp ? rope_scaled_table_kernel<1, true> : rope_scaled_table_kernel<1, false>);
   return launched(launch_pdl(kernel, dim3((unsigned)blocks), dim3(256), 0, as_stream(stream), rope_table, max_pos,
-                             half, (float)s.amplitude, rates),
+                             half, near, rho, rates),
                   "bi_rope_scaled_table");
 }
 
