@@ -409,7 +409,8 @@ class Decoder:
         set the device status (so does a sequence with more than max_nodes nodes); their ids and logprobs mean nothing.
 
         Greedy, or with `sampling` (one entry per sequence) drawn with u (fp32 [T], or a function of (row_seq, row_pos)
-        that gives it).  Every node has the bits of a decode step at the end of its path.  bf16 models only."""
+        that gives it; rows behind the last sequence have row_seq 0 and row_pos -1).  Every node has the bits of a decode
+        step at the end of its path.  bf16 models only."""
         if self.fp8:
             raise ValueError("drafted steps are built for bf16 models")
         if (sampling is None) != (u is None):
@@ -420,8 +421,15 @@ class Decoder:
                            ("block_table", block_table, max(B, block_table.shape[0]) * block_table.shape[1])):
             if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous int32 with a row per node or sequence")
-        if isinstance(u, torch.Tensor) and (u.dtype != torch.float32 or u.numel() != T or not u.is_contiguous()):
-            raise ValueError("u must be contiguous fp32 with an entry per node")
+
+        def draws(u):
+            if (not isinstance(u, torch.Tensor) or u.dtype != torch.float32 or u.numel() != T or not u.is_contiguous()
+                    or u.device != tokens.device):
+                raise ValueError("u must be contiguous fp32 with an entry per node, on the tokens' device")
+            return u
+
+        if u is not None and not callable(u):
+            draws(u)
         mb = block_table.shape[1]
 
         def buf(*shape, dtype=torch.bfloat16):
@@ -433,6 +441,8 @@ class Decoder:
         slots = torch.full((T,), -1, dtype=torch.int64, device=dev)
         L.bi_tree_slot_map(parent, n_nodes, start, B, max_nodes, block_table, mb, cache.n_blocks, T, row0, row_seq, row_pos,
                            slots)
+        if callable(u):
+            u = draws(u(row_seq, row_pos))
         h, x, tmp, q, ao = buf(T, d), buf(T, d), buf(T, d), buf(T, hq, hd), buf(T, hq * hd)
         qkv, act = buf(T, (hq + 2 * hkv) * hd), buf(T, s.ffn)
         ws = buf(L.bi_tree_attention_workspace_size(T, hq, hd, max_ctx, s.kv_split), dtype=torch.uint8)
@@ -454,8 +464,7 @@ class Decoder:
         if sampling is not None:
             logits = buf(T, s.vocab, dtype=torch.float32)
             L.bi_gemm(x, T, d, self.w["lm_head"], s.vocab, logits, L.BI_DTYPE_FP32)
-            L.bi_sample(logits, T, s.vocab, sampling, u(row_seq, row_pos) if callable(u) else u, ids, lp,
-                        param_row=row_seq)
+            L.bi_sample(logits, T, s.vocab, sampling, u, ids, lp, param_row=row_seq)
         else:
             n = L.bi_lm_head_logprob_workspace_size(T, s.vocab, d)
             L.bi_lm_head_logprob(x, T, d, self.w["lm_head"], s.vocab, None, lp, ids, workspace=buf(n, dtype=torch.uint8))
