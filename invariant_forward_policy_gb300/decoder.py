@@ -489,6 +489,13 @@ class Decoder:
         max_ctx = int(lens.max()) + n_gen + max_nodes - 1
         if -(-(max_ctx - 1) // 64) > block_table.shape[1] or int(lens.max()) + n_gen > self.max_pos:
             raise ValueError(f"drafted steps of up to {max_ctx - 1} cache positions need more blocks or RoPE rows")
+        # a block that a shorter sequence's drafts lack would read as zeros and be accepted all the same
+        table, need = block_table.cpu().numpy(), -(-(lens + n_gen + max_nodes - 2) // 64)
+        if len(table) < B:
+            raise ValueError(f"the block table has {len(table)} rows for {B} sequences")
+        for b in range(B):
+            if not ((table[b, :need[b]] >= 0) & (table[b, :need[b]] < cache.n_blocks)).all():
+                raise ValueError(f"sequence {b} lacks one of the {need[b]} blocks that its prompt, tokens and drafts need")
         if self.fp8:
             raise ValueError("drafted steps are built for bf16 models")
         last = np.cumsum(lens) - 1
