@@ -338,9 +338,11 @@ bi_status bi_attention_static_scratch(const void* q, int64_t T, const int32_t* p
  * not stand before it, or is below -1, and its descendants have position -1; a
  * cache position without a block has slot -1; both set the device status, as does
  * a sequence whose count is below 0 (taken as 0), above max_nodes, or whose rows
- * go past T: its rows are left as they were.  row_seq, row_pos, slots: NULL where
- * not wanted (block_table may be NULL without slots).  Rows behind the last
- * sequence's stay as they were. */
+ * go past T (row0 ends at T): the rows of the latter two get position and slot -1,
+ * and what a step finds for them must not be kept.  row_seq, row_pos, slots: NULL
+ * where not wanted (block_table may be NULL without slots).  Rows behind the last
+ * sequence's stay as they were: fill row_pos and slots with -1 before a call with
+ * fewer nodes than rows, or bi_rope_slot_write writes where they point. */
 bi_status bi_tree_slot_map(const int32_t* parent, const int32_t* n_nodes, const int32_t* start, int64_t B,
                            int64_t max_nodes, const int32_t* block_table, int64_t max_blocks_per_seq, int64_t n_blocks,
                            int64_t T, int32_t* row0, int32_t* row_seq, int32_t* row_pos, int64_t* slots, void* stream);

@@ -69,6 +69,12 @@ __global__ void __launch_bounds__(kSlotWarps * 32) tree_slot_map_kernel(
         slots[row] = slot;
       }
     }
+  } else {
+    // a refused sequence's rows: nothing may be written where an earlier step's rows of these buffers stood
+    for (int64_t row = first + lane; row < min(first + n, (long long)T); row += 32) {
+      if (row_pos) row_pos[row] = -1;
+      if (slots) slots[row] = -1;
+    }
   }
   if (bad) report(status, DEV_BAD_INDEX);
 }
