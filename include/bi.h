@@ -378,9 +378,10 @@ size_t bi_tree_attention_workspace_size(int64_t max_T, int Hq, int hd, int64_t m
  * caches (bf16 [n_layers, n_blocks, Hkv, 64, hd]; both or neither NULL) the j-th
  * accepted node's key and value move from position start + path[j] to start + j
  * in every layer.  A sequence without nodes, with a limit below 1, whose node 0 is
- * no root, or whose rows or start are out of range (device status) accepts none; a
- * node whose parent is not before it is no child (device status); a row whose
- * block is outside [0, n_blocks) does not move (device status). */
+ * no root, or whose rows, start or start + nodes (at most 2^31 - 1) are out of range
+ * (device status) accepts none; a node whose parent is not before it is no child
+ * (device status); a row whose block is outside [0, n_blocks) does not move (device
+ * status). */
 bi_status bi_tree_accept(const int32_t* parent, const int32_t* row0, const int32_t* start, const int32_t* tokens,
                          const int32_t* targets, const int32_t* limit, int64_t B, int64_t max_nodes, int64_t T,
                          int64_t max_path, int32_t* n_out, int32_t* path, int32_t* tokens_out, int32_t* pos_out,

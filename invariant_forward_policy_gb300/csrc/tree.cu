@@ -112,7 +112,8 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const Accep
   const bool first = blockIdx.x == 0;
   const int64_t r0 = a.row0[b], r1 = a.row0[b + 1];
   const int64_t start = a.start[b];
-  const bool fine = r0 >= 0 && r1 >= r0 && r1 <= a.T && r1 - r0 <= a.max_nodes && start >= 0;
+  const bool fine = r0 >= 0 && r1 >= r0 && r1 <= a.T && r1 - r0 <= a.max_nodes && start >= 0 &&
+                    start + (r1 - r0) <= 0x7fffffff;  // (start + m is a 32-bit position)
   const int n = fine ? (int)(r1 - r0) : 0;
   bool bad = !fine;
   int par = -1, tok = 0;
