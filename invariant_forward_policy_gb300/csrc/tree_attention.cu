@@ -47,6 +47,7 @@ struct TreeArgs {
   float neg_zero;  // -0, see mul2
 };
 
+constexpr int kMaxTailRecords = 32;  // the merge holds one a lane
 constexpr int kTreeMaxSplit = 16384;  // positions of a split (positions near max_ctx stay 32-bit numbers)
 
 // A sequence as the kernels see it: its rows, or none when its numbers cannot be right.
@@ -1067,7 +1068,6 @@ __global__ void __launch_bounds__(kTreeMergeWarps * 32) tree_merge_kernel(const 
   for (int lb = E; lb <= pos && n_tail < a.ntail; lb = lane_end(a, lb)) ++n_tail;
   float M = fmaxf(r.x, rc.x);
   if (lane < n_tail) M = fmaxf(M, rt.x);
-  for (int t = 32 + lane; t < n_tail; t += 32) M = fmaxf(M, __ldcg(tml + t).x);
   for (int s = 32 + lane; s < sE; s += 32) M = fmaxf(M, __ldcg(ml + s).x);
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float L = 0.f;
@@ -1096,8 +1096,7 @@ __global__ void __launch_bounds__(kTreeMergeWarps * 32) tree_merge_kernel(const 
   float pm = rc.x, pl = rc.y;
   int lb = E;
   for (int t = 0; t < n_tail; ++t) {
-    const float2 x = t < 32 ? make_float2(__shfl_sync(0xffffffffu, rt.x, t & 31), __shfl_sync(0xffffffffu, rt.y, t & 31))
-                            : __ldcg(tml + t);
+    const float2 x = make_float2(__shfl_sync(0xffffffffu, rt.x, t), __shfl_sync(0xffffffffu, rt.y, t));
     if (t > 0) Q = load(to + (int64_t)t * HD, true);
     if (x.x != -INFINITY) {
       if (pm == -INFINITY) {
@@ -1132,6 +1131,7 @@ __global__ void __launch_bounds__(kTreeMergeWarps * 32) tree_merge_kernel(const 
 }
 
 // Records of a row's lanes from E on: its positions there are at most `max_nodes` from anywhere in a lane.
+// At most 8 (256 nodes, a split of 832: lanes of 256 and a last one of 64).
 static int tail_records(int64_t max_nodes, int split, int lane_len) {
   const int shortest = split % lane_len ? split % lane_len : lane_len;
   return (int)((max_nodes - 1 + lane_len - 1) / shortest) + 1;
@@ -1223,6 +1223,7 @@ bi_status bi_tree_attention(const void* q, int64_t T, const int32_t* parent, con
   BI_REQUIRE(B <= 65535 && Hkv * ns <= 65535 && T <= 0x7fffffff, "too many sequences, rows or splits");
   const int lane_len = split_lane_len(kv_split);
   const int nt = tail_records(max_nodes, kv_split, lane_len);
+  BI_REQUIRE(nt <= kMaxTailRecords, "too many lanes behind the context");
   const size_t per = (size_t)T * Hq * ns, per_t = (size_t)T * Hq * nt;
   // records are written 32 bytes at a time
   const size_t skip = (32 - (reinterpret_cast<uintptr_t>(workspace) & 31)) & 31;
