@@ -188,7 +188,7 @@ __device__ __forceinline__ void tree_pv(const float (&p)[8][4], int lane, LaneSt
 
 // ------------------------------------------------------------------------ the lanes from E on
 // A warp owns a node's q heads of one kv head (a 16-row tile; groups of 32 and 64 heads take two and four warps), a
-// CTA eight neighbouring ones, whose keys and values come by TMA into its shared memory once: the pages of the first
+// CTA of four warps neighbouring ones, whose keys and values come by TMA into its shared memory once: the pages of the first
 // lane before position `start`, through a ring, then all pages that hold the tree's own keys at once.  ldmatrix takes
 // an address for every key row, so a tile behind `start` is read as if the node's path stood in the cache: the page's
 // row for a position before `start`, the path node's row behind it, a row of zeros behind the node (as a plain decode
@@ -1001,7 +1001,8 @@ __global__ void __launch_bounds__(CtxLayout<HD>::kThreads, 2)
 // lane_merge's formula.  Loads that do not depend on the row's position go out at once, and the next NB records while
 // NB are added up.  Few rows wait for their records' latency and want many in flight, many rows want the registers for
 // more warps: NB = 16, 8, 4 take 45.9, 47.6, 50.5 us a whole call for 592 rows of 64 splits, 24.6, 25.0, 25.1 for 2048
-// of one, and 168, 153.5, 150.5 for 16384 of 14.
+// of one, and 168, 153.5, 150.5 for 16384 of 14.  The rule's border (16 rows x heads an SM) lies between; nearest above
+// it 4608 rows of 2 to 64 splits: 232, 228, 227, so that there 4 and 8 are as good as each other.
 constexpr int kTreeMergeWarps = 4;
 
 template <int HD, int NB>

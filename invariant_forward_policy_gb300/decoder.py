@@ -477,7 +477,7 @@ class Decoder:
         draft(b, tokens) proposes what may follow the tokens (prompt and generated so far, int32 array) of sequence b:
         (tokens, parents) of a tree as draft_nodes takes it, ([], []) for none.  A pass scores the last token and the draft
         (at most max_nodes <= 256 nodes) and keeps the path that the model chose itself (bi_tree_accept).  Every
-        sequence needs blocks for its prompt, n_gen - 1 tokens and max_nodes - 1 drafts more."""
+        sequence needs blocks for its prompt, n_gen - 1 tokens and max_nodes - 1 drafts more (ValueError without them)."""
         B, dev, s = len(prompts), self.device, self.shape
         if (sampling is None) != (uniforms is None):
             raise ValueError("sampling and uniforms go together")
